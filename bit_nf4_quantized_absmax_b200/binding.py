@@ -8,6 +8,7 @@ not been built; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -26,6 +27,8 @@ EXPORTED = ("qlora_status_string", "qlora_nf4_codebook", "qlora_nf4_storage_byte
             "qlora_dequantize_nf4_dq", "qlora_linear_fwd", "qlora_linear_bwd", "qlora_linear_bwd_f32",
             "qlora_linear_bwd_dp", "qlora_round_bf16", "qlora_merge_lora", "qlora_codebook", "qlora_quantize_4bit",
             "qlora_dequantize_4bit", "qlora_linear_fwd_multi", "qlora_pack_adapters",
+            "qlora_mx_storage_bytes", "qlora_quantize_mx", "qlora_dequantize_mx", "qlora_rmsnorm_mx",
+            "qlora_mx_linear_fwd", "qlora_mx_grouped_fwd",
             "qlora_paged_alloc", "qlora_paged_free", "qlora_paged_prefetch", "qlora_adamw_step",
             "qlora_device_error")
 
@@ -48,6 +51,11 @@ _lib = None
 class _Adapter(ctypes.Structure):
     _fields_ = [("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("r", ctypes.c_int32), ("alpha", ctypes.c_float),
                 ("weight", ctypes.c_float)]
+
+
+class _MX(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("format", ctypes.c_int32)]
 
 
 def load_library(path: str | None = None) -> ctypes.CDLL:
@@ -85,6 +93,13 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.qlora_linear_fwd_multi.argtypes = [wp, vp, i64, vp, vp, i32, vp, vp, vp, szp, vp]
     lib.qlora_pack_adapters.argtypes = [ctypes.POINTER(_Adapter), i32, i64, i64, vp, vp, vp, vp]
     lib.qlora_merge_lora.argtypes = [wp, ctypes.POINTER(_Adapter), i32, vp, vp]
+    mp = ctypes.POINTER(_MX)
+    lib.qlora_mx_storage_bytes.argtypes = [ctypes.c_int, i64, i64, ctypes.POINTER(sz)]
+    lib.qlora_quantize_mx.argtypes = [vp, mp, vp]
+    lib.qlora_dequantize_mx.argtypes = [mp, vp, vp]
+    lib.qlora_rmsnorm_mx.argtypes = [vp, vp, vp, f32, mp, vp, vp]
+    lib.qlora_mx_linear_fwd.argtypes = [mp, mp, vp, vp]
+    lib.qlora_mx_grouped_fwd.argtypes = [mp, mp, vp, i32, vp, vp]
     lib.qlora_device_error.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
     lib.qlora_paged_alloc.argtypes = [sz, i32, ctypes.POINTER(vp)]
     lib.qlora_paged_free.argtypes = [vp]
@@ -447,6 +462,171 @@ def qlora_merge_lora(q: NF4Weight | SingleNF4Weight, adapters, out: torch.Tensor
     _check(lib.qlora_merge_lora(ctypes.byref(qc), arr, len(adapters), _ptr(out), _stream(stream)),
            "qlora_merge_lora")
     return out
+
+
+MX_E4M3, MX_E2M1 = 0, 1
+
+
+def _require(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+class MXTensor:
+    """Device storage of a matrix [rows, cols] in an MX format (MX_E4M3 or
+    MX_E2M1); the layout of `data` and `scales` is that of qlora_mx_tensor in
+    include/qlora.h. The two tensors are contiguous uint8 of the stated sizes, in
+    any shape."""
+    __slots__ = ("data", "scales", "rows", "cols", "format", "device", "_c")
+
+    def __init__(self, data: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, format: int):
+        _require(format in (MX_E4M3, MX_E2M1), f"unknown MX format {format!r}")
+        _require(rows >= 0 and cols > 0 and cols % 32 == 0, f"MX needs cols % 32 == 0, got [{rows}, {cols}]")
+        kp = (cols + 127) // 128 * 128
+        _require(data.dtype == torch.uint8 and scales.dtype == torch.uint8 and data.is_contiguous()
+                 and scales.is_contiguous() and data.device == scales.device,
+                 "MX data and scales are contiguous uint8 tensors of one device")
+        _require(data.numel() == rows * (kp // 2 if format == MX_E2M1 else kp) and scales.numel() == rows * (kp // 32),
+                 f"MX data and scales of {data.numel()} and {scales.numel()} bytes do not hold [{rows}, {cols}]")
+        self.data, self.scales, self.rows, self.cols, self.format = data, scales, rows, cols, format
+        self.device = data.device
+        self._c = _MX(data.data_ptr(), scales.data_ptr(), rows, cols, format)
+
+    def as_c(self) -> _MX:
+        return self._c
+
+    @staticmethod
+    def empty(rows: int, cols: int, format: int, device="cuda") -> "MXTensor":
+        _require(cols > 0 and cols % 32 == 0, f"MX needs cols % 32 == 0, got {cols}")
+        kp = (cols + 127) // 128 * 128
+        return MXTensor(torch.empty(rows, kp // 2 if format == MX_E2M1 else kp, dtype=torch.uint8, device=device),
+                        torch.empty(kp // 128, rows, 4, dtype=torch.uint8, device=device), rows, cols, format)
+
+
+def _on_stream(fn):
+    """With stream=s, run the call with s (and its device) current, so that what it
+    allocates belongs to s too and may be reused only in s's order."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _mx_call(name: str, device: torch.device, *args):
+    """Call an MX entry point with `device` current, on its current stream; every
+    tensor of the call is on that device."""
+    _require(device.type == "cuda", f"{name}: tensors have to be on a CUDA device, not {device}")
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    _check(status, name)
+
+
+def _mx_bf16(t: torch.Tensor, shape: tuple, device, what: str):
+    _require(t.dtype == torch.bfloat16 and tuple(t.shape) == shape and t.is_contiguous() and t.device == device,
+             f"{what} has to be a contiguous bfloat16 tensor of shape {shape} on {device}")
+
+
+def qlora_mx_storage_bytes(format: int, rows: int, cols: int) -> tuple:
+    out = (ctypes.c_size_t * 2)()
+    _check(load_library().qlora_mx_storage_bytes(format, rows, cols, out), "qlora_mx_storage_bytes")
+    return int(out[0]), int(out[1])
+
+
+@_on_stream
+def qlora_quantize_mx(X: torch.Tensor, format: int, out: MXTensor | None = None) -> MXTensor:
+    """bf16 [rows, cols] (a weight or activations) to MX blocks of 32 along the columns."""
+    _require(X.dim() == 2, "qlora_quantize_mx takes a matrix")
+    _mx_bf16(X, tuple(X.shape), X.device, "X")
+    if out is None:
+        out = MXTensor.empty(X.shape[0], X.shape[1], format, X.device)
+    _require((out.rows, out.cols) == tuple(X.shape) and out.format == format and out.device == X.device,
+             "out has another shape, format or device than X is to be quantized to")
+    _mx_call("qlora_quantize_mx", X.device, X.data_ptr(), out._c)
+    return out
+
+
+@_on_stream
+def qlora_dequantize_mx(q: MXTensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The bf16 values of an MX matrix."""
+    if out is None:
+        out = torch.empty(q.rows, q.cols, dtype=torch.bfloat16, device=q.device)
+    _mx_bf16(out, (q.rows, q.cols), q.device, "out")
+    _mx_call("qlora_dequantize_mx", q.device, q._c, out.data_ptr())
+    return out
+
+
+@_on_stream
+def qlora_rmsnorm_mx(X: torch.Tensor, gamma: torch.Tensor, eps: float, format: int = MX_E4M3,
+                     residual: torch.Tensor | None = None, out: MXTensor | None = None,
+                     residual_out: torch.Tensor | None = None):
+    """RMS norm of X + residual as MX blocks. Returns (MXTensor, the sum in bf16 or
+    None without a residual); pass residual_out=residual to update it in place."""
+    _require(X.dim() == 2, "qlora_rmsnorm_mx takes a matrix")
+    shape, dev = tuple(X.shape), X.device
+    _mx_bf16(X, shape, dev, "X")
+    _mx_bf16(gamma, shape[1:], dev, "gamma")
+    if out is None:
+        out = MXTensor.empty(shape[0], shape[1], format, dev)
+    _require((out.rows, out.cols) == shape and out.format == format and out.device == dev,
+             "out has another shape, format or device than asked for")
+    if residual is not None:
+        _mx_bf16(residual, shape, dev, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual)
+        _mx_bf16(residual_out, shape, dev, "residual_out")
+    else:
+        residual_out = None
+    _mx_call("qlora_rmsnorm_mx", dev, X.data_ptr(), None if residual is None else residual.data_ptr(),
+             gamma.data_ptr(), float(eps), out._c, None if residual is None else residual_out.data_ptr())
+    return out, residual_out
+
+
+def _mx_activations(x, w: MXTensor, x_format: int) -> MXTensor:
+    if not isinstance(x, MXTensor):
+        _require(x.dim() == 2, "activations are a matrix")
+        x = qlora_quantize_mx(x, x_format)
+    _require(x.cols == w.cols and x.device == w.device,
+             f"activations [{x.rows}, {x.cols}] do not match a weight [{w.rows}, {w.cols}] of {w.device}")
+    return x
+
+
+@_on_stream
+def qlora_mx_linear_fwd(x: MXTensor | torch.Tensor, w: MXTensor, Y: torch.Tensor | None = None,
+                        x_format: int = MX_E4M3) -> torch.Tensor:
+    """Y = x w^T (bf16) with w an MX_E2M1 weight [N, K]. x: an MXTensor [M, K], or bf16
+    activations, which are quantized to x_format first."""
+    x = _mx_activations(x, w, x_format)
+    if Y is None:
+        Y = torch.empty(x.rows, w.rows, dtype=torch.bfloat16, device=x.device)
+    _mx_bf16(Y, (x.rows, w.rows), x.device, "Y")
+    _mx_call("qlora_mx_linear_fwd", x.device, x._c, w._c, Y.data_ptr())
+    return Y
+
+
+@_on_stream
+def qlora_mx_grouped_fwd(x: MXTensor | torch.Tensor, w: MXTensor, offsets: torch.Tensor,
+                         Y: torch.Tensor | None = None, x_format: int = MX_E4M3) -> torch.Tensor:
+    """Rows offsets[e] .. offsets[e + 1] of x times expert e's weight, rows e N .. (e + 1) N
+    of w (offsets: device int32 [experts + 1]). Rows of Y outside the offsets are not
+    written. x as in qlora_mx_linear_fwd."""
+    _require(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.numel() >= 2 and offsets.is_contiguous()
+             and offsets.device == w.device, f"offsets have to be contiguous int32 [experts + 1] on {w.device}")
+    groups = offsets.numel() - 1
+    _require(w.rows > 0 and w.rows % groups == 0, f"a weight of {w.rows} rows is not {groups} experts of equal size")
+    x = _mx_activations(x, w, x_format)
+    n = w.rows // groups
+    if Y is None:
+        Y = torch.empty(x.rows, n, dtype=torch.bfloat16, device=x.device)
+    _mx_bf16(Y, (x.rows, n), x.device, "Y")
+    _mx_call("qlora_mx_grouped_fwd", x.device, x._c, w._c, offsets.data_ptr(), groups, Y.data_ptr())
+    return Y
 
 
 def qlora_device_error(stream=None) -> int:

@@ -9,6 +9,7 @@
 #include "common.cuh"
 #include "host_tables.h"
 #include "kernels.h"
+#include "mx.cuh"
 
 namespace qlora {
 __device__ int32_t g_device_error = 0;
@@ -122,6 +123,42 @@ int32_t* device_error_word() {
   void* p = nullptr;
   if (cudaGetSymbolAddress(&p, qlora::g_device_error) != cudaSuccess) return nullptr;
   return static_cast<int32_t*>(p);
+}
+
+// MX storage: sizes, format, and (for rows > 0) pointers.
+qlora_status check_mx(const qlora_mx_tensor* q) {
+  if (!q) return QLORA_ERR_INVALID_ARG;
+  if (q->rows < 0 || q->cols <= 0) return QLORA_ERR_INVALID_ARG;
+  if (q->format != QLORA_MX_E4M3 && q->format != QLORA_MX_E2M1) return QLORA_ERR_UNSUPPORTED;
+  if (q->cols % 32 || q->cols > (int64_t(1) << 30) || q->rows >= (int64_t(1) << 31)) return QLORA_ERR_UNSUPPORTED;
+  if (q->rows > 0) {
+    if (!q->data || !q->scales) return QLORA_ERR_INVALID_ARG;
+    if (!aligned(q->data, 32) || !aligned(q->scales, 4)) return QLORA_ERR_ALIGNMENT;
+  }
+  return QLORA_OK;
+}
+
+MxView mx_view(const qlora_mx_tensor* q) {
+  return MxView{q->data, q->scales, q->rows, q->cols, q->format == QLORA_MX_E2M1 ? kMxE2M1 : kMxE4M3};
+}
+
+// Dense (offsets null, one group) and grouped products.
+qlora_status mx_gemm_impl(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const int32_t* offsets, int32_t groups,
+                          void* Y, cudaStream_t stream) {
+  qlora_status st = check_mx(x);
+  if (st != QLORA_OK) return st;
+  if ((st = check_mx(w)) != QLORA_OK) return st;
+  if (w->format != QLORA_MX_E2M1) return QLORA_ERR_UNSUPPORTED;
+  if (x->cols != w->cols || w->rows == 0 || w->rows % groups) return QLORA_ERR_INVALID_ARG;
+  if (x->rows == 0) return QLORA_OK;
+  if (!Y) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(Y, 16)) return QLORA_ERR_ALIGNMENT;
+  const int64_t N = w->rows / groups;
+  if (!mx_gemm_fits(x->rows, N, groups)) return QLORA_ERR_UNSUPPORTED;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != QLORA_OK) return st;
+  return cuda_status(launch_mx_gemm(mx_view(x), mx_view(w), offsets, groups, N, Y, di.num_sms, device_error_word(),
+                                    stream));
 }
 
 // Split count for the token reductions of dA / dB: enough units to cover the SMs.
@@ -557,6 +594,67 @@ qlora_status qlora_merge_lora(const qlora_nf4_weight* q, const qlora_lora_adapte
   if ((st = device_info(&di)) != QLORA_OK) return st;
   return cuda_status(launch_merge(view(q), ma, n_adapters, W_out, quant_tables().codebook, di.num_sms,
                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qlora_status qlora_mx_storage_bytes(qlora_mx_format format, int64_t rows, int64_t cols, size_t out[2]) {
+  if (!out) return QLORA_ERR_INVALID_ARG;
+  const qlora_mx_tensor q = {nullptr, nullptr, rows, cols, format};
+  const qlora_status st = check_mx(&q);
+  if (st == QLORA_ERR_UNSUPPORTED || rows < 0 || cols <= 0) return st;  // the absent pointers are no error here
+  const size_t kp = static_cast<size_t>((cols + 127) / 128 * 128);
+  out[0] = static_cast<size_t>(rows) * (format == QLORA_MX_E2M1 ? kp / 2 : kp);
+  out[1] = static_cast<size_t>(rows) * (kp / 32);
+  return QLORA_OK;
+}
+
+qlora_status qlora_quantize_mx(const void* X_bf16, const qlora_mx_tensor* q, qlora_stream_t stream) {
+  qlora_status st = check_mx(q);
+  if (st != QLORA_OK) return st;
+  if (q->rows == 0) return QLORA_OK;
+  if (!X_bf16) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(X_bf16, 16)) return QLORA_ERR_ALIGNMENT;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != QLORA_OK) return st;
+  return cuda_status(launch_mx_quantize(X_bf16, mx_view(q), di.num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qlora_status qlora_dequantize_mx(const qlora_mx_tensor* q, void* out_bf16, qlora_stream_t stream) {
+  qlora_status st = check_mx(q);
+  if (st != QLORA_OK) return st;
+  if (q->rows == 0) return QLORA_OK;
+  if (!out_bf16) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(out_bf16, 16)) return QLORA_ERR_ALIGNMENT;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != QLORA_OK) return st;
+  return cuda_status(launch_mx_dequantize(mx_view(q), out_bf16, di.num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qlora_status qlora_rmsnorm_mx(const void* X, const void* residual, const void* gamma, float eps,
+                              const qlora_mx_tensor* q, void* residual_out, qlora_stream_t stream) {
+  qlora_status st = check_mx(q);
+  if (st != QLORA_OK) return st;
+  if (!(eps >= 0.0f)) return QLORA_ERR_INVALID_ARG;
+  if (q->cols > kMxNormMaxCols) return QLORA_ERR_UNSUPPORTED;
+  if (q->rows == 0) return QLORA_OK;
+  if (!X || !gamma || (residual && !residual_out)) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(X, 16) || !aligned(gamma, 16) || (residual && (!aligned(residual, 16) || !aligned(residual_out, 16))))
+    return QLORA_ERR_ALIGNMENT;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != QLORA_OK) return st;
+  return cuda_status(launch_rmsnorm_mx(X, residual, gamma, eps, mx_view(q), residual_out, di.num_sms,
+                                       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y, qlora_stream_t stream) {
+  return mx_gemm_impl(x, w, nullptr, 1, Y, reinterpret_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_mx_grouped_fwd(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const int32_t* offsets,
+                                  int32_t n_groups, void* Y, qlora_stream_t stream) {
+  if (!offsets || n_groups < 1) return QLORA_ERR_INVALID_ARG;
+  if (n_groups > kMxMaxGroups) return QLORA_ERR_UNSUPPORTED;
+  if (!aligned(offsets, 4)) return QLORA_ERR_ALIGNMENT;
+  return mx_gemm_impl(x, w, offsets, n_groups, Y, reinterpret_cast<cudaStream_t>(stream));
 }
 
 qlora_status qlora_device_error(int32_t* code, qlora_stream_t stream) {

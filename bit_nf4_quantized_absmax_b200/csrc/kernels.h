@@ -187,4 +187,28 @@ cudaError_t launch_zero_bf16(void* p, int64_t n, int num_sms, cudaStream_t strea
 // dst (bf16 [n]) = bf16_rn(src (fp32 [n])).
 cudaError_t launch_round_bf16(const float* src, void* dst, int64_t n, int num_sms, cudaStream_t stream);
 
+// ---- mx_quant.cu: microscaled (MX) storage ----
+struct MxView {
+  uint8_t* data;
+  uint8_t* scales;
+  int64_t rows;
+  int64_t cols;  // % 32 == 0
+  int fmt;       // kMxE4M3 or kMxE2M1 (mx.cuh)
+};
+cudaError_t launch_mx_quantize(const void* X, const MxView& q, int num_sms, cudaStream_t stream);
+cudaError_t launch_mx_dequantize(const MxView& q, void* out, int num_sms, cudaStream_t stream);
+// residual may be null (then residual_out is not written).
+constexpr int64_t kMxNormMaxCols = 32768;
+cudaError_t launch_rmsnorm_mx(const void* X, const void* residual, const void* gamma, float eps, const MxView& q,
+                              void* residual_out, int num_sms, cudaStream_t stream);
+
+// ---- mx_gemm.cu: products of MX operands on the block-scaled tensor cores ----
+// Y (bf16 [x.rows, N]): rows [offsets[e], offsets[e+1]) of x times the transpose
+// of rows [e N, (e+1) N) of w, for e < groups; offsets null: one group of all rows.
+constexpr int kMxMaxGroups = 4096;
+// Whether the product's grid and tile indices stay within their ranges.
+bool mx_gemm_fits(int64_t M, int64_t N, int64_t groups);
+cudaError_t launch_mx_gemm(const MxView& x, const MxView& w, const int32_t* offsets, int groups, int64_t N, void* Y,
+                           int num_sms, int32_t* err, cudaStream_t stream);
+
 }  // namespace qlora

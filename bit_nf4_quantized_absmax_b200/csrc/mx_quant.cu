@@ -1,0 +1,343 @@
+// Conversion of bf16 matrices to MX storage and back, and the RMS norm whose
+// output is MX. All of it is bound by memory traffic.
+//
+// Storage of [rows, cols] (cols % 32 == 0; kp = cols rounded up to 128):
+//   data   : [rows][kp] e4m3 bytes, or [rows][kp / 2] bytes of two e2m1 codes
+//            (the lower index in the low nibble); columns >= cols are code 0.
+//   scales : [kp / 128][rows][4] bytes, block kb of row r at
+//            ((kb / 4) * rows + r) * 4 + kb % 4; blocks past cols hold 127.
+// The four scale bytes that 128 elements of a row need are one 32-bit word, and
+// the words of consecutive rows are adjacent, so a GEMM stage of 128 elements
+// reads its scales in contiguous runs whatever row its tile starts at.
+#include "common.cuh"
+#include "kernels.h"
+#include "mx.cuh"
+#include "nf4_lut.cuh"
+
+namespace qlora {
+namespace {
+
+constexpr int kQuantThreads = 256;
+
+// Row and padded block of flat block index t (nkb blocks a row).
+__device__ __forceinline__ void split_index(int64_t t, int nkb, int64_t total, int64_t& row, int& kb) {
+  if (total <= 0xFFFFFFFFLL) {
+    const uint32_t r = static_cast<uint32_t>(t) / static_cast<uint32_t>(nkb);
+    row = r;
+    kb = static_cast<int>(static_cast<uint32_t>(t) - r * static_cast<uint32_t>(nkb));
+  } else {
+    row = t / nkb;
+    kb = static_cast<int>(t - row * nkb);
+  }
+}
+
+// The scale bytes of lanes 4i..4i+3 as one word (valid in lane 4i).
+__device__ __forceinline__ uint32_t gather_scale_word(uint32_t byte) {
+  uint32_t w = byte;
+  w |= __shfl_down_sync(0xffffffffu, byte, 1) << 8;
+  w |= __shfl_down_sync(0xffffffffu, byte, 2) << 16;
+  w |= __shfl_down_sync(0xffffffffu, byte, 3) << 24;
+  return w;
+}
+
+// One thread quantizes one block of 32: 64 contiguous bytes in, 32 (e4m3) or 16
+// (e2m1) out, no exchange between threads but the scale word's. The block
+// maximum is taken on the magnitude bits, two at a time, which order like the
+// values and place NaN above infinity.
+template <int FMT, bool V8>
+__global__ void __launch_bounds__(kQuantThreads)
+k_mx_quantize(const uint4* __restrict__ X, int64_t rows, int cols, uint8_t* __restrict__ data,
+              uint32_t* __restrict__ scales) {
+  pdl_enter();
+  const int kp = (cols + 127) / 128 * 128;
+  const int nkb = kp / 32, nvalid = cols / 32;
+  const int64_t total = rows * nkb;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kQuantThreads;
+  // total is a multiple of 4: the four lanes of a scale word are in range together
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kQuantThreads; t0 < total; t0 += stride) {
+    const int64_t t = t0 + threadIdx.x;
+    const bool in = t < total;
+    int64_t row = 0;
+    int kb = 0;
+    if (in) split_index(t, nkb, total, row, kb);
+    uint32_t v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0u;
+    const bool valid = in && kb < nvalid;
+    if (valid) {
+      const uint4* src = X + (row * cols + kb * 32) / 8;
+      if (V8) {
+        uint32_t a[8], b[8];
+        ld_global_cs_v8(src, a);
+        ld_global_cs_v8(src + 2, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = a[i];
+          v[8 + i] = b[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 q = __ldcs(src + i);
+          v[4 * i] = q.x;
+          v[4 * i + 1] = q.y;
+          v[4 * i + 2] = q.z;
+          v[4 * i + 3] = q.w;
+        }
+      }
+    }
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
+    m = max(m & 0xFFFFu, m >> 16);
+    const uint32_t byte = valid ? mx_scale_byte<FMT>(m >> 7) : 127u;
+    const uint32_t word = gather_scale_word(byte);
+    if (in && (threadIdx.x & 3) == 0) scales[static_cast<int64_t>(kb >> 2) * rows + row] = word;
+    if (!in) continue;
+    const bool bad = byte == 255u;
+    const float inv = mx_inverse_scale(byte);
+    if (FMT == kMxE4M3) {
+      uint32_t o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const f32x2 a = mul_f32x2({bf16lo_to_f32(v[2 * i]), bf16hi_to_f32(v[2 * i])}, {inv, inv});
+        const f32x2 b = mul_f32x2({bf16lo_to_f32(v[2 * i + 1]), bf16hi_to_f32(v[2 * i + 1])}, {inv, inv});
+        o[i] = bad ? 0u : cvt_e4m3x2(a.x, a.y) | (cvt_e4m3x2(b.x, b.y) << 16);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(data + row * kp + kb * 32);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    } else {
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x2 a = mul_f32x2({bf16lo_to_f32(v[4 * i + j]), bf16hi_to_f32(v[4 * i + j])}, {inv, inv});
+          f[2 * j] = a.x;
+          f[2 * j + 1] = a.y;
+        }
+        o[i] = bad ? 0u : cvt_e2m1x8(f);
+      }
+      *reinterpret_cast<uint4*>(data + (row * kp + kb * 32) / 2) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+// One thread decodes one block of 32 to 64 contiguous bytes of bf16. An element
+// times its scale has at most 4 significant bits, so fp32 and bf16 hold it
+// exactly except below bf16's smallest values (one rounding, nearest even). The
+// e2m1 codes go through the 16-entry table of the NF4 decoder.
+template <int FMT, bool V8>
+__global__ void __launch_bounds__(kQuantThreads)
+k_mx_dequantize(const uint8_t* __restrict__ data, const uint8_t* __restrict__ scales, int64_t rows, int cols,
+                uint4* __restrict__ out, const __grid_constant__ Nf4Codebook cb) {
+  pdl_enter();
+  const int kp = (cols + 127) / 128 * 128;
+  const int nvalid = cols / 32;
+  const int64_t total = rows * nvalid;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * kQuantThreads;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kQuantThreads + threadIdx.x; t < total; t += stride) {
+    int64_t row;
+    int kb;
+    split_index(t, nvalid, total, row, kb);
+    const float s = mx_scale(scales[(static_cast<int64_t>(kb >> 2) * rows + row) * 4 + (kb & 3)]);
+    uint32_t o[2][8];
+    if (FMT == kMxE4M3) {
+      const uint4* src = reinterpret_cast<const uint4*>(data + row * kp + kb * 32);
+      const uint4 q0 = __ldcs(src), q1 = __ldcs(src + 1);
+      const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const f32x2 a = mul_f32x2(e4m3x2_to_f32x2(w[i]), {s, s});
+        const f32x2 b = mul_f32x2(e4m3x2_to_f32x2(w[i] >> 16), {s, s});
+        o[i >> 2][2 * (i & 3)] = pack_bf16x2(a.x, a.y);
+        o[i >> 2][2 * (i & 3) + 1] = pack_bf16x2(b.x, b.y);
+      }
+    } else {
+      const uint4 q = __ldcs(reinterpret_cast<const uint4*>(data + (row * kp + kb * 32) / 2));
+      const Nf4Lut lut = make_nf4_lut(cb, s);
+      nf4_lookup8(lut, q.x, o[0]);
+      nf4_lookup8(lut, q.y, o[0] + 4);
+      nf4_lookup8(lut, q.z, o[1]);
+      nf4_lookup8(lut, q.w, o[1] + 4);
+    }
+    uint4* dst = out + (row * cols + kb * 32) / 8;
+    if (V8) {
+      st_global_cs_v8(dst, o[0]);
+      st_global_cs_v8(dst + 2, o[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        __stcs(dst + i, make_uint4(o[i >> 1][4 * (i & 1)], o[i >> 1][4 * (i & 1) + 1], o[i >> 1][4 * (i & 1) + 2],
+                                   o[i >> 1][4 * (i & 1) + 3]));
+    }
+  }
+}
+
+// h = bf16(x + residual) (or x), rstd = 1 / sqrt(mean(h^2) + eps), y = h rstd
+// gamma, y to MX blocks: one CTA a row, the row read once and kept in registers
+// (8 elements a chunk, CHUNKS chunks a thread), so x and the residual cross
+// memory once in and the sum and the codes once out.
+//
+// The squares of bf16 values are exact in fp32; a thread adds at most 32 of them
+// in fp32 and the rest of the sum, the mean and rstd are fp64 (a few operations
+// a row). h * gamma is exact in fp32 too, and rstd enters as a head and a tail,
+// so y carries one fp32 rounding before it is quantized. Four neighbouring
+// lanes hold a block; the sixteen lanes of 128 elements make a scale word.
+template <int FMT, int CHUNKS, bool RES>
+__global__ void __launch_bounds__(1024)
+k_rmsnorm_mx(const uint4* __restrict__ X, const uint4* residual, const uint4* __restrict__ gamma, float eps,
+             int64_t rows, int cols, uint4* residual_out, uint8_t* __restrict__ data, uint32_t* __restrict__ scales) {
+  __shared__ double warp_sum[32];
+  const int T = blockDim.x;
+  const int kp = (cols + 127) / 128 * 128;
+  const int nchunk = cols / 8, nchunk_p = kp / 8;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_enter();
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const int64_t base = row * nchunk;
+    // every load of the row before the first store: residual_out may be residual
+    uint4 xq[CHUNKS], rq[CHUNKS];
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int i = c * T + threadIdx.x;
+      xq[c] = rq[c] = make_uint4(0u, 0u, 0u, 0u);
+      if (i < nchunk) {
+        xq[c] = __ldcs(X + base + i);
+        if (RES) rq[c] = __ldcs(residual + base + i);
+      }
+    }
+    uint32_t h[CHUNKS][4];
+    float ss = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int i = c * T + threadIdx.x;
+      h[c][0] = xq[c].x;
+      h[c][1] = xq[c].y;
+      h[c][2] = xq[c].z;
+      h[c][3] = xq[c].w;
+      if (RES) {
+        const uint32_t rr[4] = {rq[c].x, rq[c].y, rq[c].z, rq[c].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          h[c][j] = pack_bf16x2(bf16lo_to_f32(h[c][j]) + bf16lo_to_f32(rr[j]),
+                                bf16hi_to_f32(h[c][j]) + bf16hi_to_f32(rr[j]));
+        if (i < nchunk) residual_out[base + i] = make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = bf16lo_to_f32(h[c][j]), b = bf16hi_to_f32(h[c][j]);
+        ss = __fmaf_rn(a, a, ss);
+        ss = __fmaf_rn(b, b, ss);
+      }
+    }
+    double d = ss;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+    if (lane == 0) warp_sum[warp] = d;
+    __syncthreads();
+    d = 0.0;
+    for (int w = 0; w < T / 32; ++w) d += warp_sum[w];  // the same order in every thread
+    __syncthreads();                                    // before the next row writes it
+    const double rstd = 1.0 / sqrt(d / cols + static_cast<double>(eps));
+    const float r_hi = static_cast<float>(rstd);
+    const float r_lo = static_cast<float>(rstd - static_cast<double>(r_hi));
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+      const int i = c * T + threadIdx.x;
+      const bool valid = i < nchunk;
+      uint4 g = make_uint4(0u, 0u, 0u, 0u);
+      if (valid) g = __ldg(gamma + i);
+      const uint32_t gg[4] = {g.x, g.y, g.z, g.w};
+      float y[8];
+      uint32_t m = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = bf16lo_to_f32(h[c][j]) * bf16lo_to_f32(gg[j]);
+        const float b = bf16hi_to_f32(h[c][j]) * bf16hi_to_f32(gg[j]);
+        y[2 * j] = valid ? __fmaf_rn(a, r_hi, a * r_lo) : 0.0f;
+        y[2 * j + 1] = valid ? __fmaf_rn(b, r_hi, b * r_lo) : 0.0f;
+        m = max(m, max(__float_as_uint(y[2 * j]) & 0x7FFFFFFFu, __float_as_uint(y[2 * j + 1]) & 0x7FFFFFFFu));
+      }
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const uint32_t byte = valid ? mx_scale_byte<FMT>(m >> 23) : 127u;
+      uint32_t word = byte;
+      word |= __shfl_down_sync(0xffffffffu, byte, 4) << 8;
+      word |= __shfl_down_sync(0xffffffffu, byte, 8) << 16;
+      word |= __shfl_down_sync(0xffffffffu, byte, 12) << 24;
+      if (i >= nchunk_p) continue;
+      if ((lane & 15) == 0) scales[static_cast<int64_t>(i >> 4) * rows + row] = word;
+      const float inv = mx_inverse_scale(byte);
+      const bool bad = byte == 255u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] *= inv;
+      if (FMT == kMxE4M3) {
+        uint2 o = make_uint2(cvt_e4m3x2(y[0], y[1]) | (cvt_e4m3x2(y[2], y[3]) << 16),
+                             cvt_e4m3x2(y[4], y[5]) | (cvt_e4m3x2(y[6], y[7]) << 16));
+        if (bad) o = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2*>(data + row * kp + static_cast<int64_t>(i) * 8) = o;
+      } else {
+        *reinterpret_cast<uint32_t*>(data + (row * kp + static_cast<int64_t>(i) * 8) / 2) = bad ? 0u : cvt_e2m1x8(y);
+      }
+    }
+  }
+}
+
+int flat_grid(int64_t threads, int num_sms) {
+  const int64_t want = (threads + kQuantThreads - 1) / kQuantThreads;
+  const int64_t cap = static_cast<int64_t>(num_sms) * 32;
+  return static_cast<int>(want < cap ? (want > 0 ? want : 1) : cap);
+}
+
+template <int FMT, bool RES>
+cudaError_t run_rmsnorm(const void* X, const void* residual, const void* gamma, float eps, const MxView& q,
+                        void* residual_out, int num_sms, cudaStream_t stream) {
+  const int nchunk_p = static_cast<int>((q.cols + 127) / 128 * 16);
+  int chunks = 1;
+  while (nchunk_p > 1024 * chunks) chunks *= 2;
+  const int threads = ((nchunk_p + chunks - 1) / chunks + 31) / 32 * 32;
+  const int64_t cap = static_cast<int64_t>(num_sms) * 64;
+  const int grid = static_cast<int>(q.rows < cap ? q.rows : cap);
+  auto kern = chunks == 1 ? k_rmsnorm_mx<FMT, 1, RES> : (chunks == 2 ? k_rmsnorm_mx<FMT, 2, RES> : k_rmsnorm_mx<FMT, 4, RES>);
+  return launch_pdl(kern, dim3(grid), dim3(threads), 0, stream, reinterpret_cast<const uint4*>(X),
+                    reinterpret_cast<const uint4*>(residual), reinterpret_cast<const uint4*>(gamma), eps, q.rows,
+                    static_cast<int>(q.cols), reinterpret_cast<uint4*>(residual_out), q.data,
+                    reinterpret_cast<uint32_t*>(q.scales));
+}
+
+}  // namespace
+
+cudaError_t launch_mx_quantize(const void* X, const MxView& q, int num_sms, cudaStream_t stream) {
+  const bool v8 = (reinterpret_cast<uintptr_t>(X) & 31u) == 0;
+  auto kern = q.fmt == kMxE4M3 ? (v8 ? k_mx_quantize<kMxE4M3, true> : k_mx_quantize<kMxE4M3, false>)
+                               : (v8 ? k_mx_quantize<kMxE2M1, true> : k_mx_quantize<kMxE2M1, false>);
+  const int64_t blocks = q.rows * ((q.cols + 127) / 128 * 4);
+  return launch_pdl(kern, dim3(flat_grid(blocks, num_sms)), dim3(kQuantThreads), 0, stream,
+                    reinterpret_cast<const uint4*>(X), q.rows, static_cast<int>(q.cols), q.data,
+                    reinterpret_cast<uint32_t*>(q.scales));
+}
+
+cudaError_t launch_mx_dequantize(const MxView& q, void* out, int num_sms, cudaStream_t stream) {
+  // code order of e2m1: sign in bit 3
+  const Nf4Codebook cb = {{0.0f, 0.5f, 1.0f, 1.5f, 2.0f, 3.0f, 4.0f, 6.0f, -0.0f, -0.5f, -1.0f, -1.5f, -2.0f, -3.0f,
+                           -4.0f, -6.0f}};
+  const bool v8 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+  auto kern = q.fmt == kMxE4M3 ? (v8 ? k_mx_dequantize<kMxE4M3, true> : k_mx_dequantize<kMxE4M3, false>)
+                               : (v8 ? k_mx_dequantize<kMxE2M1, true> : k_mx_dequantize<kMxE2M1, false>);
+  return launch_pdl(kern, dim3(flat_grid(q.rows * (q.cols / 32), num_sms)), dim3(kQuantThreads), 0, stream,
+                    q.data, q.scales, q.rows, static_cast<int>(q.cols), reinterpret_cast<uint4*>(out), cb);
+}
+
+cudaError_t launch_rmsnorm_mx(const void* X, const void* residual, const void* gamma, float eps, const MxView& q,
+                              void* residual_out, int num_sms, cudaStream_t stream) {
+  if (q.fmt == kMxE4M3)
+    return residual ? run_rmsnorm<kMxE4M3, true>(X, residual, gamma, eps, q, residual_out, num_sms, stream)
+                    : run_rmsnorm<kMxE4M3, false>(X, residual, gamma, eps, q, residual_out, num_sms, stream);
+  return residual ? run_rmsnorm<kMxE2M1, true>(X, residual, gamma, eps, q, residual_out, num_sms, stream)
+                  : run_rmsnorm<kMxE2M1, false>(X, residual, gamma, eps, q, residual_out, num_sms, stream);
+}
+
+}  // namespace qlora

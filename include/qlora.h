@@ -12,7 +12,11 @@
  *      forward and backward (dX, dA, dB; W stays frozen, no dW),
  *   6. merging weighted LoRA adapters into the base weight,
  *   7. paged AdamW for the LoRA parameters (optimizer state in managed memory
- *      that pages between GPU and CPU).
+ *      that pages between GPU and CPU),
+ *   8. serving a merged weight in the 4-bit format that the tensor cores
+ *      multiply directly: microscaled (MX) quantization, products of MX
+ *      activations with MXFP4 weights (dense, and grouped by expert), and an
+ *      RMS norm whose output is MX.
  *
  * Sources (web pages describing the method; no code is printed on them):
  *   [G]  "Guanaco" (chipfoundryservices.com/topic/guanaco), sections
@@ -43,7 +47,8 @@
  *     Workspace contents need no initialisation and are not preserved.
  *   - The library keeps no state between calls and may be used from several
  *     host threads at once (on distinct workspaces).
- *   - Inputs must be finite; non-finite weights give unspecified codes.
+ *   - Inputs must be finite; non-finite weights give unspecified codes (the MX
+ *     calls say what they do with non-finite values).
  *   - s = (float)alpha / (float)r, one fp32 division.
  */
 #ifndef QLORA_B200_H
@@ -425,6 +430,104 @@ qlora_status qlora_linear_fwd_multi(const qlora_nf4_weight* q, const void* X, in
 qlora_status qlora_pack_adapters(const qlora_lora_adapter* adapters, int32_t n_adapters, int64_t rows,
                                  int64_t cols, void* A_cat, void* B_cat, float* col_scale,
                                  qlora_stream_t stream);
+
+/* Microscaled (MX) formats: 32 consecutive elements of a row share a scale 2^e,
+ * stored as the byte e + 127 (255 is NaN). QLORA_MX_E4M3: 8-bit elements with 4
+ * exponent and 3 mantissa bits (largest value 448). QLORA_MX_E2M1: 4-bit elements
+ * with 2 and 1 (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6; bit 3 is the sign, and a
+ * code is the float's bits, not an index into a codebook as in QLORA_DTYPE_FP4).
+ * Both are the element types that the tensor cores of an sm_100a GPU multiply
+ * with block scales applied. (The pages name the 4-bit float; the block format is
+ * the public OCP microscaling one.) */
+typedef enum {
+  QLORA_MX_E4M3 = 0,
+  QLORA_MX_E2M1 = 1
+} qlora_mx_format;
+
+/* MX storage of a matrix [rows, cols], cols % 32 == 0. With kp = cols rounded up
+ * to a multiple of 128:
+ *   data   : E4M3: [rows, kp] bytes. E2M1: [rows, kp / 2] bytes, element 2i in
+ *            the low nibble of byte i. Columns cols .. kp - 1 hold code 0.
+ *   scales : [kp / 128, rows, 4] bytes: block kb (columns 32 kb .. 32 kb + 31) of
+ *            row r at ((kb / 4) * rows + r) * 4 + kb % 4. Blocks past cols hold 127.
+ * Device memory owned by the caller, data aligned to 32 bytes, scales to 4.
+ * 0 <= rows < 2^31, 32 <= cols <= 2^30. Storage written by others (an imported
+ * checkpoint) has to keep the padding as stated: the products read it. */
+typedef struct {
+  uint8_t* data;
+  uint8_t* scales;
+  int64_t  rows;
+  int64_t  cols;
+  int32_t  format;  /* qlora_mx_format */
+} qlora_mx_tensor;
+
+/* qlora_mx_storage_bytes -- bytes of data (out[0]) and scales (out[1]) of an MX
+ * matrix [rows, cols] (host call). Errors: INVALID_ARG (NULL out, negative rows,
+ * cols <= 0), UNSUPPORTED (unknown format, cols % 32 != 0, sizes out of range). */
+qlora_status qlora_mx_storage_bytes(qlora_mx_format format, int64_t rows, int64_t cols, size_t out[2]);
+
+/* qlora_quantize_mx -- bf16 X [q->rows, q->cols] to MX, padding included. Per
+ * block of 32: amax = max |x|; e = max(floor(log2 amax) - emax, -127) with emax = 8
+ * (E4M3) or 2 (E2M1), and e = -127 for amax = 0; the element is x 2^-e rounded to
+ * the element type (nearest, ties to even), saturated at its largest value. A
+ * block that holds an infinity or a NaN gets scale byte 255 and codes 0, so it
+ * decodes to NaN and any product that reads it is NaN. The outputs are exact
+ * functions of x. Weights and activations use the same call; n_groups experts of
+ * [N, K] are quantized as one matrix [n_groups * N, K]. rows == 0 writes nothing.
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA, DEVICE. */
+qlora_status qlora_quantize_mx(const void* X_bf16, const qlora_mx_tensor* q, qlora_stream_t stream);
+
+/* qlora_dequantize_mx -- element * 2^e to bf16 out [q->rows, q->cols] (16-byte
+ * aligned). Exact, except that results below bf16's smallest normal number are
+ * rounded to its subnormal ones (nearest, ties to even).
+ * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA, DEVICE. */
+qlora_status qlora_dequantize_mx(const qlora_mx_tensor* q, void* out_bf16, qlora_stream_t stream);
+
+/* qlora_rmsnorm_mx -- RMS norm of bf16 rows, with the residual's addition before
+ * it and MX blocks after it, for the projection that follows:
+ *   h = bf16_rn(X + residual)   (h = X when residual is NULL), to residual_out
+ *   y = h / sqrt(mean(h^2) + eps) * gamma, quantized to q as qlora_quantize_mx
+ *       does (from the unrounded y).
+ *   X            : device bf16 [q->rows, q->cols]; q->cols <= 32768.
+ *   residual     : device bf16 of X's shape, or NULL.
+ *   residual_out : device bf16 of X's shape; may be `residual` itself (an update
+ *                  in place). Required with a residual, ignored without one.
+ *   gamma        : device bf16 [q->cols].   eps >= 0.
+ * The mean and the root are evaluated in fp64 from fp32 partial sums of at most 32
+ * squares (which overflow for |h| above about 10^18), y carries one fp32 rounding.
+ * A row that holds an infinity or a NaN, or only zeros with eps == 0, quantizes to
+ * NaN where its y is not finite. rows == 0 writes nothing.
+ * Errors: INVALID_ARG (also eps < 0 or NaN), UNSUPPORTED, ALIGNMENT, CUDA, DEVICE. */
+qlora_status qlora_rmsnorm_mx(const void* X, const void* residual, const void* gamma, float eps,
+                              const qlora_mx_tensor* q, void* residual_out, qlora_stream_t stream);
+
+/* qlora_mx_linear_fwd -- Y = x w^T on the block-scaled tensor cores.
+ *   x : MX [M, K], either format (from qlora_rmsnorm_mx or qlora_quantize_mx).
+ *   w : MX [N, K], QLORA_MX_E2M1 (else UNSUPPORTED).
+ *   Y : device bf16 [M, N] (16-byte aligned).
+ * Products are exact and summed in fp32; Y is rounded once. A NaN block makes its
+ * row (of x) or column (of w) of Y NaN. The result does not depend on the other
+ * rows of x; how the sum over K is split depends on the sizes alone, so equal
+ * calls give equal bits. M == 0 writes nothing.
+ * Errors: INVALID_ARG (also x->cols != w->cols, w->rows == 0), UNSUPPORTED,
+ * ALIGNMENT, CUDA, DEVICE. */
+qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y,
+                                 qlora_stream_t stream);
+
+/* qlora_mx_grouped_fwd -- qlora_mx_linear_fwd grouped by expert: rows
+ * offsets[e] .. offsets[e + 1] - 1 of x times the transpose of expert e's weight,
+ * rows e N .. (e + 1) N - 1 of w, for 0 <= e < n_groups, N = w->rows / n_groups.
+ *   offsets : device int32 [n_groups + 1], not decreasing, read on the device by
+ *             the call's kernel (no host copy, so the call can be captured and
+ *             replayed with other offsets). Empty groups are allowed. Rows outside
+ *             [offsets[0], offsets[n_groups]) of Y are left as they were. Values
+ *             outside [0, M] or decreasing are treated as the nearest that are
+ *             not: no memory outside the arguments is touched.
+ *   1 <= n_groups <= 4096; w->rows % n_groups == 0; M * n_groups tiles must fit the
+ *   launch (else UNSUPPORTED).
+ * The rest as in qlora_mx_linear_fwd. */
+qlora_status qlora_mx_grouped_fwd(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const int32_t* offsets,
+                                  int32_t n_groups, void* Y, qlora_stream_t stream);
 
 /* qlora_paged_alloc -- allocate `bytes` of paged memory for optimizer state
  * ([C] 4: a unified pool that pages between GPU and CPU memory, so the state

@@ -1,0 +1,177 @@
+"""CPU checks of the MX calls: the oracle against its definition, storage sizes,
+and every refusal of the C entry points and of the binding. Nothing is launched."""
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from bit_nf4_quantized_absmax_b200 import binding as b
+from oracle import mx
+
+
+def test_oracle_element_values():
+    assert mx.MAGNITUDES[mx.E2M1].tolist() == [0, 0.5, 1, 1.5, 2, 3, 4, 6]
+    t = mx.MAGNITUDES[mx.E4M3]
+    assert t[1] == 2.0 ** -9 and t[8] == 2.0 ** -6 and t[-1] == 448 and len(t) == 127
+    ours = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(t, ours)
+
+
+@pytest.mark.parametrize("fmt", [mx.E4M3, mx.E2M1])
+def test_oracle_rounding(fmt):
+    """Every element value encodes to itself, midpoints go to the even code, and random values to a nearest one."""
+    t = mx.MAGNITUDES[fmt]
+    assert np.array_equal(mx.encode(t, fmt), np.arange(len(t)))
+    mid = (t[:-1] + t[1:]) / 2
+    assert np.all(mx.encode(mid, fmt) % 2 == 0)
+    rng = np.random.default_rng(0)
+    v = rng.normal(size=2000) * t[-1] / 2
+    got = mx.decode(mx.encode(v, fmt), fmt)
+    both = np.concatenate([-t, t])
+    best = np.abs(np.clip(v, -t[-1], t[-1])[:, None] - both).min(1)
+    assert np.array_equal(np.abs(np.clip(v, -t[-1], t[-1]) - got), best)
+    assert mx.encode(np.array([1e9, -1e9]), fmt).tolist() == [len(t) - 1, len(t) - 1 + mx.SIGN[fmt]]
+
+
+@pytest.mark.parametrize("fmt", [mx.E4M3, mx.E2M1])
+def test_oracle_blocks(fmt):
+    """Quantizing decoded values gives them back, a block's largest value keeps its binade, a zero block has byte 0 and
+    a block with an infinity or NaN decodes to NaN."""
+    rng = np.random.default_rng(1)
+    x = rng.normal(size=(4, 96)) * 2.0 ** rng.integers(-30, 30, size=(4, 96))
+    x[0, :32] = 0.0
+    codes, sc = mx.quantize(x, fmt)
+    v = mx.dequantize(codes, sc, fmt)
+    assert sc[0, 0] == 0 and not v[0, :32].any()
+    c2, s2 = mx.quantize(v, fmt)
+    assert np.array_equal(mx.dequantize(c2, s2, fmt), v)
+    big = np.abs(x).reshape(4, 3, 32).max(-1)
+    kept = np.abs(v).reshape(4, 3, 32).max(-1)
+    assert np.all(kept <= 2 * big) and np.all(kept >= big * 0.75 - 1e-300)  # 6 / 8: saturation takes a quarter at most
+    x[1, 33], x[2, 64] = np.nan, -np.inf
+    v = mx.dequantize(*mx.quantize(x, fmt), fmt)
+    assert np.isnan(v[1, 32:64]).all() and np.isnan(v[2, 64:]).all() and np.isfinite(v[0]).all()
+    d, s = mx.pack(codes, sc, fmt)
+    got = mx.unpack(d, s, 4, 96, fmt)
+    assert np.array_equal(got[0], codes) and np.array_equal(got[1], sc)
+    assert s.shape == (1, 4, 4) and np.all(s[0, :, 3] == 127)
+
+
+def test_storage_bytes():
+    assert b.qlora_mx_storage_bytes(b.MX_E2M1, 11008, 4096) == (11008 * 2048, 11008 * 128)
+    assert b.qlora_mx_storage_bytes(b.MX_E4M3, 3, 160) == (3 * 256, 3 * 8)  # rows padded to 256 columns
+    assert b.qlora_mx_storage_bytes(b.MX_E4M3, 0, 32) == (0, 0)
+    for args, status in (((7, 4, 64), 2), ((0, 4, 48), 2), ((0, -1, 64), 1), ((0, 4, 0), 1), ((0, 1 << 31, 64), 2),
+                         ((0, 4, (1 << 30) + 32), 2)):
+        with pytest.raises(b.QloraError) as e:
+            b.qlora_mx_storage_bytes(*args)
+        assert e.value.status == status, args
+    assert b.load_library().qlora_mx_storage_bytes(0, 4, 64, None) == 1
+
+
+P = 1 << 20  # an aligned non-null dummy
+
+
+def _mx(rows=8, cols=128, fmt=b.MX_E4M3, data=P, scales=P):
+    return b._MX(data, scales, rows, cols, fmt)
+
+
+def test_refusals_of_the_c_calls():
+    """Each returns its status before anything is launched (there is no device here: a call that got further would
+    return QLORA_ERR_CUDA)."""
+    lib = b.load_library()
+    ok = _mx()
+    bad = [(_mx(rows=-1), 1), (_mx(cols=0), 1), (_mx(cols=48), 2), (_mx(fmt=2), 2), (_mx(fmt=-1), 2),
+           (_mx(rows=1 << 31), 2), (_mx(data=None), 1), (_mx(scales=None), 1), (_mx(data=P + 16), 3),
+           (_mx(scales=P + 2), 3)]
+    w = _mx(rows=64, fmt=b.MX_E2M1)
+    for q, status in bad:
+        r = ctypes.byref(q)
+        assert lib.qlora_quantize_mx(P, r, None) == status
+        assert lib.qlora_dequantize_mx(r, P, None) == status
+        assert lib.qlora_rmsnorm_mx(P, None, P, 1e-5, r, None, None) == status
+        assert lib.qlora_mx_linear_fwd(r, ctypes.byref(w), P, None) == status
+        assert lib.qlora_mx_grouped_fwd(r, ctypes.byref(w), P, 4, P, None) == status
+        if q.format != b.MX_E4M3 or status != 2:
+            continue
+        assert lib.qlora_mx_linear_fwd(ctypes.byref(ok), r, P, None) == status
+    r, rw = ctypes.byref(ok), ctypes.byref(w)
+    assert lib.qlora_quantize_mx(P, None, None) == 1
+    assert lib.qlora_quantize_mx(None, r, None) == 1
+    assert lib.qlora_quantize_mx(P + 8, r, None) == 3
+    assert lib.qlora_dequantize_mx(r, None, None) == 1
+    assert lib.qlora_dequantize_mx(r, P + 2, None) == 3
+    norm = lib.qlora_rmsnorm_mx
+    assert norm(P, None, P, -1e-5, r, None, None) == 1
+    assert norm(P, None, P, float("nan"), r, None, None) == 1
+    assert norm(None, None, P, 1e-5, r, None, None) == 1
+    assert norm(P, None, None, 1e-5, r, None, None) == 1
+    assert norm(P, P, P, 1e-5, r, None, None) == 1             # a residual needs residual_out
+    assert norm(P, P, P, 1e-5, r, P + 8, None) == 3
+    assert norm(P, P + 4, P, 1e-5, r, P, None) == 3
+    assert norm(P, None, P, 1e-5, ctypes.byref(_mx(cols=32768 + 32)), None, None) == 2
+    fwd, grp = lib.qlora_mx_linear_fwd, lib.qlora_mx_grouped_fwd
+    assert fwd(r, r, P, None) == 2                              # the weight has to be E2M1
+    assert fwd(r, ctypes.byref(_mx(rows=64, cols=256, fmt=b.MX_E2M1)), P, None) == 1
+    assert fwd(r, ctypes.byref(_mx(rows=0, fmt=b.MX_E2M1)), P, None) == 1
+    assert fwd(None, rw, P, None) == 1 and fwd(r, None, P, None) == 1
+    assert fwd(r, rw, None, None) == 1 and fwd(r, rw, P + 2, None) == 3
+    assert grp(r, rw, None, 4, P, None) == 1
+    assert grp(r, rw, P, 0, P, None) == 1
+    assert grp(r, rw, P + 1, 4, P, None) == 3
+    assert grp(r, rw, P, 4097, P, None) == 2
+    assert grp(r, rw, P, 5, P, None) == 1                       # 64 rows are not 5 experts
+    many = _mx(rows=(1 << 31) - 1)
+    assert fwd(ctypes.byref(many), ctypes.byref(_mx(rows=(1 << 31) - 1, fmt=b.MX_E2M1)), P, None) == 2
+    # no rows: nothing to do, and the pointers are not looked at
+    none = ctypes.byref(_mx(rows=0, data=None, scales=None))
+    assert lib.qlora_quantize_mx(None, none, None) == 0 and lib.qlora_dequantize_mx(none, None, None) == 0
+    assert norm(None, None, None, 1e-5, none, None, None) == 0
+    assert fwd(none, rw, None, None) == 0 and grp(none, rw, P, 4, None, None) == 0
+
+
+def _tensors(rows, cols, fmt, device="cpu"):
+    return b.MXTensor.empty(rows, cols, fmt, device)
+
+
+def test_refusals_of_the_binding():
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    with pytest.raises(ValueError):
+        b.MXTensor.empty(4, 48, b.MX_E4M3, "cpu")
+    with pytest.raises(ValueError):
+        b.MXTensor.empty(4, 64, 5, "cpu")
+    d, s = torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(1, 4, 4, dtype=torch.uint8)
+    b.MXTensor(d, s, 4, 64, b.MX_E4M3)
+    for bad in ((d[:, :64], s), (d.to(torch.int8), s), (d, s[:, :2].contiguous()), (d[:3], s), (d.t(), s)):
+        with pytest.raises(ValueError):
+            b.MXTensor(*bad, 4, 64, b.MX_E4M3)
+    w = _tensors(64, 128, b.MX_E2M1)
+    x = _tensors(4, 128, b.MX_E4M3)
+    calls = [
+        lambda: b.qlora_quantize_mx(bf(4, 128).float(), b.MX_E4M3),
+        lambda: b.qlora_quantize_mx(bf(4, 256)[:, ::2], b.MX_E4M3),
+        lambda: b.qlora_quantize_mx(bf(128), b.MX_E4M3),
+        lambda: b.qlora_quantize_mx(bf(4, 100), b.MX_E4M3),
+        lambda: b.qlora_quantize_mx(bf(4, 128), b.MX_E4M3, out=w),
+        lambda: b.qlora_quantize_mx(bf(4, 128), b.MX_E4M3),                    # not on a GPU
+        lambda: b.qlora_dequantize_mx(x, out=bf(4, 64)),
+        lambda: b.qlora_dequantize_mx(x),
+        lambda: b.qlora_rmsnorm_mx(bf(4, 128), bf(64), 1e-5),
+        lambda: b.qlora_rmsnorm_mx(bf(4, 128), bf(128), 1e-5, residual=bf(3, 128)),
+        lambda: b.qlora_rmsnorm_mx(bf(4, 128), bf(128), 1e-5, residual=bf(4, 128), residual_out=bf(4, 64)),
+        lambda: b.qlora_rmsnorm_mx(bf(4, 128), bf(128), 1e-5, out=w),
+        lambda: b.qlora_mx_linear_fwd(_tensors(4, 64, b.MX_E4M3), w),
+        lambda: b.qlora_mx_linear_fwd(x, w, Y=bf(4, 32)),
+        lambda: b.qlora_mx_linear_fwd(x, w),
+        lambda: b.qlora_mx_grouped_fwd(x, w, torch.zeros(5)),
+        lambda: b.qlora_mx_grouped_fwd(x, w, torch.zeros(1, dtype=torch.int32)),
+        lambda: b.qlora_mx_grouped_fwd(x, w, torch.zeros(6, dtype=torch.int32)),
+        lambda: b.qlora_mx_grouped_fwd(x, w, torch.zeros(10, dtype=torch.int32)[::2]),
+    ]
+    for k, call in enumerate(calls):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {k} was not refused")
