@@ -28,7 +28,7 @@ EXPORTED = ("qlora_status_string", "qlora_nf4_codebook", "qlora_nf4_storage_byte
             "qlora_linear_bwd_dp", "qlora_round_bf16", "qlora_merge_lora", "qlora_codebook", "qlora_quantize_4bit",
             "qlora_dequantize_4bit", "qlora_linear_fwd_multi", "qlora_pack_adapters",
             "qlora_mx_storage_bytes", "qlora_quantize_mx", "qlora_dequantize_mx", "qlora_rmsnorm_mx",
-            "qlora_mx_linear_fwd", "qlora_mx_grouped_fwd",
+            "qlora_mx_linear_fwd", "qlora_mx_linear_fwd_bf16", "qlora_mx_grouped_fwd", "qlora_mx_grouped_fwd_bf16",
             "qlora_paged_alloc", "qlora_paged_free", "qlora_paged_prefetch", "qlora_adamw_step",
             "qlora_device_error")
 
@@ -99,7 +99,9 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.qlora_dequantize_mx.argtypes = [mp, vp, vp]
     lib.qlora_rmsnorm_mx.argtypes = [vp, vp, vp, f32, mp, vp, vp]
     lib.qlora_mx_linear_fwd.argtypes = [mp, mp, vp, vp]
+    lib.qlora_mx_linear_fwd_bf16.argtypes = [vp, i64, ctypes.c_int, mp, vp, vp, szp, vp]
     lib.qlora_mx_grouped_fwd.argtypes = [mp, mp, vp, i32, vp, vp]
+    lib.qlora_mx_grouped_fwd_bf16.argtypes = [vp, i64, ctypes.c_int, mp, vp, i32, vp, vp, szp, vp]
     lib.qlora_device_error.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
     lib.qlora_paged_alloc.argtypes = [sz, i32, ctypes.POINTER(vp)]
     lib.qlora_paged_free.argtypes = [vp]
@@ -466,41 +468,78 @@ def qlora_merge_lora(q: NF4Weight | SingleNF4Weight, adapters, out: torch.Tensor
 
 MX_E4M3, MX_E2M1 = 0, 1
 
+# The current stream's handle without a Stream object (0.1 against 3 us a call, of about 10).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _require(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
 
 
+def _mx_bytes(rows: int, cols: int, format: int) -> tuple:
+    """Bytes of data and scales (qlora_mx_storage_bytes, without a call)."""
+    if not (format == MX_E4M3 or format == MX_E2M1):
+        raise ValueError(f"unknown MX format {format!r}")
+    if cols <= 0 or cols % 32 or rows < 0:
+        raise ValueError(f"MX storage needs cols % 32 == 0, got [{rows}, {cols}]")
+    kp = (cols + 127) // 128 * 128
+    return rows * (kp // 2 if format == MX_E2M1 else kp), rows * (kp // 32)
+
+
 class MXTensor:
     """Device storage of a matrix [rows, cols] in an MX format (MX_E4M3 or
     MX_E2M1); the layout of `data` and `scales` is that of qlora_mx_tensor in
-    include/qlora.h. The two tensors are contiguous uint8 of the stated sizes, in
-    any shape."""
-    __slots__ = ("data", "scales", "rows", "cols", "format", "device", "_c")
+    include/qlora.h. Made from two contiguous uint8 tensors of the stated sizes in
+    any shape, or with MXTensor.empty, which allocates both at once."""
+    __slots__ = ("_data", "_scales", "rows", "cols", "format", "device", "_c")
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, format: int):
-        _require(format in (MX_E4M3, MX_E2M1), f"unknown MX format {format!r}")
-        _require(rows >= 0 and cols > 0 and cols % 32 == 0, f"MX needs cols % 32 == 0, got [{rows}, {cols}]")
-        kp = (cols + 127) // 128 * 128
+        nd, ns = _mx_bytes(rows, cols, format)
         _require(data.dtype == torch.uint8 and scales.dtype == torch.uint8 and data.is_contiguous()
                  and scales.is_contiguous() and data.device == scales.device,
                  "MX data and scales are contiguous uint8 tensors of one device")
-        _require(data.numel() == rows * (kp // 2 if format == MX_E2M1 else kp) and scales.numel() == rows * (kp // 32),
-                 f"MX data and scales of {data.numel()} and {scales.numel()} bytes do not hold [{rows}, {cols}]")
-        self.data, self.scales, self.rows, self.cols, self.format = data, scales, rows, cols, format
+        if data.numel() != nd or scales.numel() != ns:
+            raise ValueError(f"data and scales of {data.numel()} and {scales.numel()} bytes do not hold "
+                             f"[{rows}, {cols}] ({nd} and {ns} bytes)")
+        self._data, self._scales, self.rows, self.cols, self.format = data, scales, rows, cols, format
         self.device = data.device
         self._c = _MX(data.data_ptr(), scales.data_ptr(), rows, cols, format)
 
     def as_c(self) -> _MX:
         return self._c
 
+    @property
+    def data(self) -> torch.Tensor:
+        """uint8 [rows, kp] (E4M3) or [rows, kp / 2] (E2M1)."""
+        if self._scales is None:
+            self._split()
+        return self._data
+
+    @property
+    def scales(self) -> torch.Tensor:
+        """uint8 [kp / 128, rows, 4]."""
+        if self._scales is None:
+            self._split()
+        return self._scales
+
+    def _split(self):
+        buf = self._data
+        nd, _ = _mx_bytes(self.rows, self.cols, self.format)
+        kp = (self.cols + 127) // 128 * 128
+        self._data = buf[:nd].view(self.rows, kp // 2 if self.format == MX_E2M1 else kp)
+        self._scales = buf[nd:].view(kp // 128, self.rows, 4)
+
     @staticmethod
     def empty(rows: int, cols: int, format: int, device="cuda") -> "MXTensor":
-        _require(cols > 0 and cols % 32 == 0, f"MX needs cols % 32 == 0, got {cols}")
-        kp = (cols + 127) // 128 * 128
-        return MXTensor(torch.empty(rows, kp // 2 if format == MX_E2M1 else kp, dtype=torch.uint8, device=device),
-                        torch.empty(kp // 128, rows, 4, dtype=torch.uint8, device=device), rows, cols, format)
+        nd, ns = _mx_bytes(rows, cols, format)  # nd is a multiple of 64
+        buf = torch.empty(nd + ns, dtype=torch.uint8, device=device)
+        q = MXTensor.__new__(MXTensor)
+        q._data, q._scales, q.rows, q.cols, q.format, q.device = buf, None, rows, cols, format, buf.device
+        p = buf.data_ptr()
+        q._c = _MX(p, p + nd, rows, cols, format)
+        return q
 
 
 def _on_stream(fn):
@@ -518,19 +557,30 @@ def _on_stream(fn):
 def _mx_call(name: str, device: torch.device, *args):
     """Call an MX entry point with `device` current, on its current stream; every
     tensor of the call is on that device."""
-    _require(device.type == "cuda", f"{name}: tensors have to be on a CUDA device, not {device}")
-    fn = getattr(load_library(), name)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if device.type != "cuda":
+        raise ValueError(f"{name}: tensors have to be on a CUDA device, not {device}")
+    fn = getattr(_lib or load_library(), name)
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
-    _check(status, name)
+            status = fn(*args, _raw_stream(index))
+    if status != QLORA_OK:
+        raise QloraError(status, name)
 
 
 def _mx_bf16(t: torch.Tensor, shape: tuple, device, what: str):
-    _require(t.dtype == torch.bfloat16 and tuple(t.shape) == shape and t.is_contiguous() and t.device == device,
-             f"{what} has to be a contiguous bfloat16 tensor of shape {shape} on {device}")
+    if t.dtype != torch.bfloat16 or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what} has to be a contiguous bfloat16 tensor of shape {tuple(shape)} on {device}")
+
+
+def _mx_out(out: MXTensor | None, shape: tuple, format: int, device) -> MXTensor:
+    if out is None:
+        return MXTensor.empty(shape[0], shape[1], format, device)
+    if out.rows != shape[0] or out.cols != shape[1] or out.format != format or out.device != device:
+        raise ValueError("out has another shape, format or device than the result")
+    return out
 
 
 def qlora_mx_storage_bytes(format: int, rows: int, cols: int) -> tuple:
@@ -542,13 +592,12 @@ def qlora_mx_storage_bytes(format: int, rows: int, cols: int) -> tuple:
 @_on_stream
 def qlora_quantize_mx(X: torch.Tensor, format: int, out: MXTensor | None = None) -> MXTensor:
     """bf16 [rows, cols] (a weight or activations) to MX blocks of 32 along the columns."""
-    _require(X.dim() == 2, "qlora_quantize_mx takes a matrix")
-    _mx_bf16(X, tuple(X.shape), X.device, "X")
-    if out is None:
-        out = MXTensor.empty(X.shape[0], X.shape[1], format, X.device)
-    _require((out.rows, out.cols) == tuple(X.shape) and out.format == format and out.device == X.device,
-             "out has another shape, format or device than X is to be quantized to")
-    _mx_call("qlora_quantize_mx", X.device, X.data_ptr(), out._c)
+    shape, dev = X.shape, X.device
+    if len(shape) != 2:
+        raise ValueError("qlora_quantize_mx takes a matrix")
+    _mx_bf16(X, shape, dev, "X")
+    out = _mx_out(out, shape, format, dev)
+    _mx_call("qlora_quantize_mx", dev, X.data_ptr(), out._c)
     return out
 
 
@@ -557,7 +606,8 @@ def qlora_dequantize_mx(q: MXTensor, out: torch.Tensor | None = None) -> torch.T
     """The bf16 values of an MX matrix."""
     if out is None:
         out = torch.empty(q.rows, q.cols, dtype=torch.bfloat16, device=q.device)
-    _mx_bf16(out, (q.rows, q.cols), q.device, "out")
+    else:
+        _mx_bf16(out, (q.rows, q.cols), q.device, "out")
     _mx_call("qlora_dequantize_mx", q.device, q._c, out.data_ptr())
     return out
 
@@ -568,46 +618,74 @@ def qlora_rmsnorm_mx(X: torch.Tensor, gamma: torch.Tensor, eps: float, format: i
                      residual_out: torch.Tensor | None = None):
     """RMS norm of X + residual as MX blocks. Returns (MXTensor, the sum in bf16 or
     None without a residual); pass residual_out=residual to update it in place."""
-    _require(X.dim() == 2, "qlora_rmsnorm_mx takes a matrix")
-    shape, dev = tuple(X.shape), X.device
+    shape, dev = X.shape, X.device
+    if len(shape) != 2:
+        raise ValueError("qlora_rmsnorm_mx takes a matrix")
     _mx_bf16(X, shape, dev, "X")
     _mx_bf16(gamma, shape[1:], dev, "gamma")
-    if out is None:
-        out = MXTensor.empty(shape[0], shape[1], format, dev)
-    _require((out.rows, out.cols) == shape and out.format == format and out.device == dev,
-             "out has another shape, format or device than asked for")
-    if residual is not None:
+    if residual is None:
+        residual_out = rp = op = None
+    else:
         _mx_bf16(residual, shape, dev, "residual")
         if residual_out is None:
             residual_out = torch.empty_like(residual)
-        _mx_bf16(residual_out, shape, dev, "residual_out")
-    else:
-        residual_out = None
-    _mx_call("qlora_rmsnorm_mx", dev, X.data_ptr(), None if residual is None else residual.data_ptr(),
-             gamma.data_ptr(), float(eps), out._c, None if residual is None else residual_out.data_ptr())
+        else:
+            _mx_bf16(residual_out, shape, dev, "residual_out")
+        rp, op = residual.data_ptr(), residual_out.data_ptr()
+    out = _mx_out(out, shape, format, dev)
+    _mx_call("qlora_rmsnorm_mx", dev, X.data_ptr(), rp, gamma.data_ptr(), eps, out._c, op)
     return out, residual_out
 
 
-def _mx_activations(x, w: MXTensor, x_format: int) -> MXTensor:
-    if not isinstance(x, MXTensor):
-        _require(x.dim() == 2, "activations are a matrix")
-        x = qlora_quantize_mx(x, x_format)
-    _require(x.cols == w.cols and x.device == w.device,
-             f"activations [{x.rows}, {x.cols}] do not match a weight [{w.rows}, {w.cols}] of {w.device}")
-    return x
+_mx_need = {}      # workspace bytes by call and sizes, as the library's size query answers
+_mx_untouched = {}  # device: 256 bytes that stand for the workspace of calls that use none of it
+
+
+def _mx_workspace(name: str, device, x_format: int, rows: int, w: MXTensor, grouped: tuple) -> torch.Tensor:
+    key = (name, x_format, rows, w.rows, w.cols, grouped[1:])
+    need = _mx_need.get(key)
+    if need is None:
+        size = ctypes.c_size_t(0)
+        _mx_call(name, device, None, rows, x_format, w._c, *grouped, None, None, ctypes.byref(size))
+        if len(_mx_need) >= 4096:
+            _mx_need.clear()
+        need = _mx_need[key] = size.value
+    if need > 256:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    ws = _mx_untouched.get(device)
+    if ws is None:
+        ws = _mx_untouched[device] = torch.empty(256, dtype=torch.uint8, device=device)
+    return ws
+
+
+def _mx_product(name: str, x, w: MXTensor, n: int, Y, x_format: int, *grouped) -> torch.Tensor:
+    """The two products' common part: x an MXTensor, or bf16 activations for the quantizing entry point."""
+    dev = w.device
+    mx = isinstance(x, MXTensor)
+    rows, cols = (x.rows, x.cols) if mx else x.shape if x.dim() == 2 else (-1, -1)
+    if cols != w.cols or x.device != dev:
+        raise ValueError(f"{name}: activations [{rows}, {cols}] on {x.device} do not match a weight "
+                         f"[{w.rows}, {w.cols}] on {dev}")
+    if Y is None:
+        Y = torch.empty(rows, n, dtype=torch.bfloat16, device=dev)
+    else:
+        _mx_bf16(Y, (rows, n), dev, "Y")
+    if mx:
+        _mx_call(name, dev, x._c, w._c, *grouped, Y.data_ptr())
+        return Y
+    _mx_bf16(x, (rows, cols), dev, "x")
+    ws = _mx_workspace(name + "_bf16", dev, x_format, rows, w, grouped)
+    _mx_call(name + "_bf16", dev, x.data_ptr(), rows, x_format, w._c, *grouped, Y.data_ptr(), ws.data_ptr(),
+             ctypes.byref(ctypes.c_size_t(ws.numel())))
+    return Y
 
 
 @_on_stream
 def qlora_mx_linear_fwd(x: MXTensor | torch.Tensor, w: MXTensor, Y: torch.Tensor | None = None,
                         x_format: int = MX_E4M3) -> torch.Tensor:
     """Y = x w^T (bf16) with w an MX_E2M1 weight [N, K]. x: an MXTensor [M, K], or bf16
-    activations, which are quantized to x_format first."""
-    x = _mx_activations(x, w, x_format)
-    if Y is None:
-        Y = torch.empty(x.rows, w.rows, dtype=torch.bfloat16, device=x.device)
-    _mx_bf16(Y, (x.rows, w.rows), x.device, "Y")
-    _mx_call("qlora_mx_linear_fwd", x.device, x._c, w._c, Y.data_ptr())
-    return Y
+    activations, which the call quantizes to x_format first."""
+    return _mx_product("qlora_mx_linear_fwd", x, w, w.rows, Y, x_format)
 
 
 @_on_stream
@@ -616,17 +694,13 @@ def qlora_mx_grouped_fwd(x: MXTensor | torch.Tensor, w: MXTensor, offsets: torch
     """Rows offsets[e] .. offsets[e + 1] of x times expert e's weight, rows e N .. (e + 1) N
     of w (offsets: device int32 [experts + 1]). Rows of Y outside the offsets are not
     written. x as in qlora_mx_linear_fwd."""
-    _require(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.numel() >= 2 and offsets.is_contiguous()
-             and offsets.device == w.device, f"offsets have to be contiguous int32 [experts + 1] on {w.device}")
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous() \
+            or offsets.device != w.device:
+        raise ValueError(f"offsets have to be contiguous int32 [experts + 1] on {w.device}")
     groups = offsets.numel() - 1
-    _require(w.rows > 0 and w.rows % groups == 0, f"a weight of {w.rows} rows is not {groups} experts of equal size")
-    x = _mx_activations(x, w, x_format)
-    n = w.rows // groups
-    if Y is None:
-        Y = torch.empty(x.rows, n, dtype=torch.bfloat16, device=x.device)
-    _mx_bf16(Y, (x.rows, n), x.device, "Y")
-    _mx_call("qlora_mx_grouped_fwd", x.device, x._c, w._c, offsets.data_ptr(), groups, Y.data_ptr())
-    return Y
+    if w.rows == 0 or w.rows % groups:
+        raise ValueError(f"a weight of {w.rows} rows is not {groups} experts of equal size")
+    return _mx_product("qlora_mx_grouped_fwd", x, w, w.rows // groups, Y, x_format, offsets.data_ptr(), groups)
 
 
 def qlora_device_error(stream=None) -> int:

@@ -125,6 +125,17 @@ int32_t* device_error_word() {
   return static_cast<int32_t*>(p);
 }
 
+// Workspace layout: consecutive 256-byte aligned regions.
+struct Layout {
+  size_t off = 0;
+  size_t add(size_t bytes) {
+    const size_t o = off;
+    off += align_up(bytes);
+    return o;
+  }
+  size_t total() const { return off > 0 ? off : kAlign; }
+};
+
 // MX storage: sizes, format, and (for rows > 0) pointers.
 qlora_status check_mx(const qlora_mx_tensor* q) {
   if (!q) return QLORA_ERR_INVALID_ARG;
@@ -142,23 +153,68 @@ MxView mx_view(const qlora_mx_tensor* q) {
   return MxView{q->data, q->scales, q->rows, q->cols, q->format == QLORA_MX_E2M1 ? kMxE2M1 : kMxE4M3};
 }
 
-// Dense (offsets null, one group) and grouped products.
-qlora_status mx_gemm_impl(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const int32_t* offsets, int32_t groups,
-                          void* Y, cudaStream_t stream) {
+// Checks shared by the products; x may lack its storage (x_bf16 stands for it).
+qlora_status check_mx_product(const qlora_mx_tensor* w, int64_t M, int64_t K, int32_t groups, bool grouped,
+                              const int32_t* offsets) {
+  if (grouped) {
+    if (!offsets || groups < 1) return QLORA_ERR_INVALID_ARG;
+    if (groups > kMxMaxGroups) return QLORA_ERR_UNSUPPORTED;
+    if (!aligned(offsets, 4)) return QLORA_ERR_ALIGNMENT;
+  }
+  const qlora_status st = check_mx(w);
+  if (st != QLORA_OK) return st;
+  if (w->format != QLORA_MX_E2M1) return QLORA_ERR_UNSUPPORTED;
+  if (K != w->cols || w->rows == 0 || w->rows % groups) return QLORA_ERR_INVALID_ARG;
+  return mx_gemm_fits(M, w->rows / groups, groups) ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
+}
+
+// Dense (offsets null, one group) and grouped products of MX activations.
+qlora_status mx_product_impl(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const int32_t* offsets,
+                             int32_t groups, bool grouped, void* Y, qlora_stream_t stream) {
   qlora_status st = check_mx(x);
   if (st != QLORA_OK) return st;
-  if ((st = check_mx(w)) != QLORA_OK) return st;
-  if (w->format != QLORA_MX_E2M1) return QLORA_ERR_UNSUPPORTED;
-  if (x->cols != w->cols || w->rows == 0 || w->rows % groups) return QLORA_ERR_INVALID_ARG;
+  if ((st = check_mx_product(w, x->rows, x->cols, groups, grouped, offsets)) != QLORA_OK) return st;
   if (x->rows == 0) return QLORA_OK;
   if (!Y) return QLORA_ERR_INVALID_ARG;
   if (!aligned(Y, 16)) return QLORA_ERR_ALIGNMENT;
-  const int64_t N = w->rows / groups;
-  if (!mx_gemm_fits(x->rows, N, groups)) return QLORA_ERR_UNSUPPORTED;
   DeviceInfo di;
   if ((st = device_info(&di)) != QLORA_OK) return st;
-  return cuda_status(launch_mx_gemm(mx_view(x), mx_view(w), offsets, groups, N, Y, di.num_sms, device_error_word(),
-                                    stream));
+  return cuda_status(launch_mx_gemm(mx_view(x), nullptr, mx_view(w), offsets, groups, w->rows / groups, Y, di.num_sms,
+                                    device_error_word(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// The same from bf16 activations: quantized in the product's kernel, or before it into the workspace.
+qlora_status mx_product_bf16_impl(const void* X, int64_t M, qlora_mx_format x_format, const qlora_mx_tensor* w,
+                                  const int32_t* offsets, int32_t groups, bool grouped, void* Y, void* workspace,
+                                  size_t* workspace_bytes, qlora_stream_t stream) {
+  if (!w || M < 0) return QLORA_ERR_INVALID_ARG;
+  if (x_format != QLORA_MX_E4M3 && x_format != QLORA_MX_E2M1) return QLORA_ERR_UNSUPPORTED;
+  if (M >= (int64_t(1) << 31)) return QLORA_ERR_UNSUPPORTED;
+  qlora_status st = check_mx_product(w, M, w->cols, groups, grouped, offsets);
+  if (st != QLORA_OK) return st;
+  MxView x{nullptr, nullptr, M, w->cols, x_format == QLORA_MX_E2M1 ? kMxE2M1 : kMxE4M3};
+  const bool inside = mx_gemm_quantizes(M, grouped ? groups : 1);
+  const size_t kp = static_cast<size_t>((w->cols + 127) / 128 * 128);
+  Layout L;
+  const size_t off_data = inside ? 0 : L.add(static_cast<size_t>(M) * (x.fmt == kMxE2M1 ? kp / 2 : kp));
+  const size_t off_scales = inside ? 0 : L.add(static_cast<size_t>(M) * (kp / 32));
+  bool launch = false;
+  st = workspace_check(workspace, workspace_bytes, L.total(), &launch);
+  if (st != QLORA_OK || !launch) return st;
+  if (M == 0) return QLORA_OK;
+  if (!X || !Y) return QLORA_ERR_INVALID_ARG;
+  if (!aligned(X, 16) || !aligned(Y, 16)) return QLORA_ERR_ALIGNMENT;
+  DeviceInfo di;
+  if ((st = device_info(&di)) != QLORA_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (!inside) {
+    x.data = static_cast<uint8_t*>(workspace) + off_data;
+    x.scales = static_cast<uint8_t*>(workspace) + off_scales;
+    const cudaError_t e = launch_mx_quantize(X, x, di.num_sms, cs);
+    if (e != cudaSuccess) return QLORA_ERR_CUDA;
+  }
+  return cuda_status(launch_mx_gemm(x, inside ? X : nullptr, mx_view(w), offsets, groups, w->rows / groups, Y,
+                                    di.num_sms, device_error_word(), cs));
 }
 
 // Split count for the token reductions of dA / dB: enough units to cover the SMs.
@@ -178,17 +234,6 @@ int red_splits(int64_t M, int rpad, int64_t Kred, int num_sms) {
   const int64_t sp = (2 * num_sms) / tiles;  // at most one round of the two resident CTAs per SM
   return split_count(nkb, static_cast<int>(sp < 1 ? 1 : sp));
 }
-
-// Workspace layout: consecutive 256-byte aligned regions.
-struct Layout {
-  size_t off = 0;
-  size_t add(size_t bytes) {
-    const size_t o = off;
-    off += align_up(bytes);
-    return o;
-  }
-  size_t total() const { return off > 0 ? off : kAlign; }
-};
 
 // Backward shared by qlora_linear_bwd (bf16 dA, dB), qlora_linear_bwd_f32 and
 // qlora_linear_bwd_dp (fp32 dA, dB). The LoRA gradients are finished before the
@@ -646,15 +691,23 @@ qlora_status qlora_rmsnorm_mx(const void* X, const void* residual, const void* g
 }
 
 qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y, qlora_stream_t stream) {
-  return mx_gemm_impl(x, w, nullptr, 1, Y, reinterpret_cast<cudaStream_t>(stream));
+  return mx_product_impl(x, w, nullptr, 1, false, Y, stream);
+}
+
+qlora_status qlora_mx_linear_fwd_bf16(const void* X, int64_t M, qlora_mx_format x_format, const qlora_mx_tensor* w,
+                                      void* Y, void* workspace, size_t* workspace_bytes, qlora_stream_t stream) {
+  return mx_product_bf16_impl(X, M, x_format, w, nullptr, 1, false, Y, workspace, workspace_bytes, stream);
 }
 
 qlora_status qlora_mx_grouped_fwd(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const int32_t* offsets,
                                   int32_t n_groups, void* Y, qlora_stream_t stream) {
-  if (!offsets || n_groups < 1) return QLORA_ERR_INVALID_ARG;
-  if (n_groups > kMxMaxGroups) return QLORA_ERR_UNSUPPORTED;
-  if (!aligned(offsets, 4)) return QLORA_ERR_ALIGNMENT;
-  return mx_gemm_impl(x, w, offsets, n_groups, Y, reinterpret_cast<cudaStream_t>(stream));
+  return mx_product_impl(x, w, offsets, n_groups, true, Y, stream);
+}
+
+qlora_status qlora_mx_grouped_fwd_bf16(const void* X, int64_t M, qlora_mx_format x_format, const qlora_mx_tensor* w,
+                                       const int32_t* offsets, int32_t n_groups, void* Y, void* workspace,
+                                       size_t* workspace_bytes, qlora_stream_t stream) {
+  return mx_product_bf16_impl(X, M, x_format, w, offsets, n_groups, true, Y, workspace, workspace_bytes, stream);
 }
 
 qlora_status qlora_device_error(int32_t* code, qlora_stream_t stream) {

@@ -205,10 +205,12 @@ cudaError_t launch_rmsnorm_mx(const void* X, const void* residual, const void* g
 // ---- mx_gemm.cu: products of MX operands on the block-scaled tensor cores ----
 // Y (bf16 [x.rows, N]): rows [offsets[e], offsets[e+1]) of x times the transpose
 // of rows [e N, (e+1) N) of w, for e < groups; offsets null: one group of all rows.
+// x_bf16, where mx_gemm_quantizes() says so, stands for x's storage.
 constexpr int kMxMaxGroups = 4096;
 // Whether the product's grid and tile indices stay within their ranges.
 bool mx_gemm_fits(int64_t M, int64_t N, int64_t groups);
-cudaError_t launch_mx_gemm(const MxView& x, const MxView& w, const int32_t* offsets, int groups, int64_t N, void* Y,
-                           int num_sms, int32_t* err, cudaStream_t stream);
+bool mx_gemm_quantizes(int64_t M, int64_t groups);
+cudaError_t launch_mx_gemm(const MxView& x, const void* x_bf16, const MxView& w, const int32_t* offsets, int groups,
+                           int64_t N, void* Y, int num_sms, int32_t* err, cudaStream_t stream);
 
 }  // namespace qlora

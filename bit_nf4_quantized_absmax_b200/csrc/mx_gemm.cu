@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kMxBK = 128;     // elements of k a stage
 constexpr int kMxRows = 128;   // weight rows a tile
-constexpr int kMxThreads = 128;
+constexpr int kMxThreads = 128;   // and four warps more where the kernel quantizes x
 
 template <int TN>
 struct MxCfg {
@@ -148,24 +148,107 @@ __device__ __forceinline__ TokenTile find_token_tile(const int32_t* __restrict__
 }
 
 struct MxArgs {
+  const uint4* x_bf16;     // QUANT: activations still to be quantized, [M, K]
   const uint8_t* x_scales;
   const uint8_t* w_scales;
   const int32_t* offsets;  // null: one group of all M rows
   int groups;
   int64_t M, N, w_rows;
-  int n_tiles, nkb;
+  int n_tiles, nkb, K;
   uint32_t idesc;
   bool x_fp4;  // the widening copies of e2m1 count the bytes of codes, not of containers
   __nv_bfloat16* Y;
 };
+
+// The tokens' side of the stages, from bf16 (warps 4..7 of the QUANT kernel).
+template <int TN, int FMT>
+__device__ __forceinline__ void quantize_stages(const MxArgs& a, int64_t row0, int tokens, int kb0, int kb1,
+                                                uint8_t* smem, uint64_t* full, uint64_t* empty,
+                                                volatile int* abort_flag, int32_t* err) {
+  using C = MxCfg<TN>;
+  static_assert(TN * 8 == 128, "a thread holds 16 elements of a stage");
+  constexpr int AHEAD = 4;
+  const int t = threadIdx.x - kMxThreads;
+  const int row = t >> 3, h = t & 7;  // token, and which 16 of the stage's 128 elements
+  const bool mine = row < tokens;
+  const uint4* src = a.x_bf16 + ((row0 + (mine ? row : 0)) * a.K + h * 16) / 8;
+  uint4 q[AHEAD][2];
+  auto load = [&](int kb, uint4 (&d)[2]) {
+    d[0] = d[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (mine && kb < kb1 && kb * kMxBK + h * 16 < a.K) {
+      d[0] = __ldg(src + kb * (kMxBK / 8));
+      d[1] = __ldg(src + kb * (kMxBK / 8) + 1);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) load(kb0 + i, q[i]);
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int base = kb0; base < kb1; base += AHEAD) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int kb = base + i;
+      if (kb >= kb1) return;
+      const uint32_t v[8] = {q[i][0].x, q[i][0].y, q[i][0].z, q[i][0].w, q[i][1].x, q[i][1].y, q[i][1].z, q[i][1].w};
+      load(kb + AHEAD, q[i]);
+      uint32_t m = 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = __vmaxu2(m, v[j] & 0x7FFF7FFFu);
+      m = max(m & 0xFFFFu, m >> 16);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));  // the block's other half
+      const uint32_t byte = mx_scale_byte<FMT>(m >> 7);
+      const float inv = mx_inverse_scale(byte);
+      float f[16];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const f32x2 p = mul_f32x2({bf16lo_to_f32(v[j]), bf16hi_to_f32(v[j])}, {inv, inv});
+        f[2 * j] = p.x;
+        f[2 * j + 1] = p.y;
+      }
+      const bool bad = byte == 255u;
+      if (!__all_sync(0xffffffffu, wait_or_abort(&empty[stage], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY)))
+        return;
+      uint8_t* sx = smem + stage * C::STAGE_BYTES + C::W_BYTES;
+      if (mine) {
+        uint8_t* dst = sx + row * 128 + ((h ^ (row & 7)) << 4);  // 128-byte swizzle
+        if (FMT == kMxE4M3) {
+          uint4 o;
+          o.x = cvt_e4m3x2(f[0], f[1]) | (cvt_e4m3x2(f[2], f[3]) << 16);
+          o.y = cvt_e4m3x2(f[4], f[5]) | (cvt_e4m3x2(f[6], f[7]) << 16);
+          o.z = cvt_e4m3x2(f[8], f[9]) | (cvt_e4m3x2(f[10], f[11]) << 16);
+          o.w = cvt_e4m3x2(f[12], f[13]) | (cvt_e4m3x2(f[14], f[15]) << 16);
+          *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0u, 0u, 0u, 0u) : o;
+        } else {
+          const float lo[8] = {f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]};
+          const float hi[8] = {f[8], f[9], f[10], f[11], f[12], f[13], f[14], f[15]};
+          *reinterpret_cast<uint2*>(dst) = bad ? make_uint2(0u, 0u) : make_uint2(cvt_e2m1x8(lo), cvt_e2m1x8(hi));
+        }
+        if ((h & 1) == 0) sx[C::X_BYTES + 512 + row * 16 + (h >> 1)] = static_cast<uint8_t>(byte);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&full[stage]);
+      if (++stage == C::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+}
 
 // One tile a cluster of S CTAs, CTA r of the cluster taking k-blocks [r nkb / S,
 // (r + 1) nkb / S). Warp 0 issues the TMA copies, warp 1 the MMAs, warps 2 and 3
 // the scale words of the weights and the tokens; all four then drain the
 // accumulator. With S > 1 each CTA leaves its fp32 partial in shared memory and
 // adds up its share of the tokens over the cluster, in the order of the CTAs.
-template <int TN>
-__global__ void __launch_bounds__(kMxThreads)
+//
+// QUANT (TN = 16): x is bf16, and four more warps write the tokens' side of a stage
+// themselves: thread t holds 16 elements, half an MX block, of token t / 8, four
+// stages ahead in registers, so that a decode step is one launch and its
+// activations are never stored. A few tokens are quantized again by every CTA,
+// which costs less than a launch and a round trip through memory.
+template <int TN, bool QUANT>
+__global__ void __launch_bounds__(QUANT ? kMxThreads + 128 : kMxThreads)
 k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const MxArgs a,
           int32_t* err) {
   using C = MxCfg<TN>;
@@ -185,14 +268,14 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 3);  // the TMA warp and the two scale warps
+      mbar_init(&full[s], QUANT ? 6 : 3);  // the TMA warp, the scale warp(s), the four quantizing warps
       mbar_init(&empty[s], 1);
     }
     mbar_init(accf, 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&tm_w);
-    prefetch_tmap(&tm_x);
+    if (!QUANT) prefetch_tmap(&tm_x);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
@@ -227,9 +310,9 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
             break;
           }
           uint8_t* sw = smem + stage * C::STAGE_BYTES;
-          mbar_arrive_expect_tx(&full[stage], C::W_BYTES / 2 + (a.x_fp4 ? C::X_BYTES / 2 : C::X_BYTES));
+          mbar_arrive_expect_tx(&full[stage], C::W_BYTES / 2 + (QUANT ? 0 : a.x_fp4 ? C::X_BYTES / 2 : C::X_BYTES));
           tma_load_2d(sw, &tm_w, &full[stage], kb * kMxBK, static_cast<int32_t>(w0));
-          tma_load_2d(sw + C::W_BYTES, &tm_x, &full[stage], kb * kMxBK, static_cast<int32_t>(tt.row0));
+          if (!QUANT) tma_load_2d(sw + C::W_BYTES, &tm_x, &full[stage], kb * kMxBK, static_cast<int32_t>(tt.row0));
           outstanding |= 1u << stage;
           out_parity = (out_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == C::STAGES) {
@@ -273,7 +356,15 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
         }
         if (ok) mma_commit(accf);
       }
-    } else {
+    } else if (QUANT && warp >= 4) {
+      if constexpr (QUANT) {
+        const int tokens = static_cast<int>(min(static_cast<int64_t>(TN), tt.end - tt.row0));
+        if (a.x_fp4)
+          quantize_stages<TN, kMxE2M1>(a, tt.row0, tokens, kb0, kb1, smem, full, empty, abort_flag, err);
+        else
+          quantize_stages<TN, kMxE4M3>(a, tt.row0, tokens, kb0, kb1, smem, full, empty, abort_flag, err);
+      }
+    } else if (!QUANT || warp == 2) {
       // scale words of 128 weight rows (warp 2) or TN tokens (warp 3)
       constexpr int LAG = 2;  // stages in flight behind the one being issued
       const bool wside = warp == 2;
@@ -327,9 +418,9 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     tc_fence_after();
     const int64_t n = n0 + threadIdx.x;  // lane of TMEM = weight row
     const int tokens = static_cast<int>(min(static_cast<int64_t>(TN), tt.end - tt.row0));
-    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+    const uint32_t tacc = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     float* part = reinterpret_cast<float*>(smem);
-    if (__all_sync(0xffffffffu, ok)) {
+    if (warp < 4 && __all_sync(0xffffffffu, ok)) {
 #pragma unroll 1
       for (int c = 0; c < TN; c += 32) {
         float v[32];
@@ -348,7 +439,7 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     }
     if (S > 1) {
       cluster_sync_all();
-      if (!*abort_flag) {
+      if (warp < 4 && !*abort_flag) {
         const uint32_t mine = smem_u32(part) + threadIdx.x * 4;
         for (int j = rank; j < tokens; j += S) {
           float sum = 0.0f;
@@ -385,21 +476,27 @@ bool make_mx_map(CUtensorMap* m, const MxView& v, int box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TN>
+template <int TN, bool QUANT = false>
 cudaError_t run_tiles(const MxView& x, const MxView& w, MxArgs a, int64_t tok_tiles, int num_sms, int32_t* err,
                       cudaStream_t stream) {
   using C = MxCfg<TN>;
   CUtensorMap tw, tx;
-  if (!make_mx_map(&tw, w, kMxRows) || !make_mx_map(&tx, x, TN)) return cudaErrorInvalidValue;
+  if (!make_mx_map(&tw, w, kMxRows)) return cudaErrorInvalidValue;
+  if (QUANT)
+    tx = tw;  // not used
+  else if (!make_mx_map(&tx, x, TN))
+    return cudaErrorInvalidValue;
   a.idesc = mx_instr_desc(kFmtE2M1, x.fmt == kMxE2M1 ? kFmtE2M1 : kFmtE4M3, kMxRows, TN);
   const int64_t tiles = tok_tiles * a.n_tiles;
-  int S = 1;  // CTAs a tile: as many as fit on the card at once with at least 4 stages of work each
-  while (S < 8 && tiles * S * 2 <= 2 * num_sms && a.nkb >= 8 * S) S *= 2;
-  cudaError_t e = ensure_smem_limit<k_mx_gemm<TN>>(C::SMEM);
+  // CTAs a tile: as many as are on the card at once, with at least 4 stages of work each
+  int S = static_cast<int>(2 * num_sms / tiles < 8 ? 2 * num_sms / tiles : 8);
+  if (S > a.nkb / 4) S = a.nkb / 4;
+  if (S < 1) S = 1;
+  cudaError_t e = ensure_smem_limit<k_mx_gemm<TN, QUANT>>(C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
-  cfg.blockDim = dim3(kMxThreads);
+  cfg.blockDim = dim3(QUANT ? kMxThreads + 128 : kMxThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -411,7 +508,7 @@ cudaError_t run_tiles(const MxView& x, const MxView& w, MxArgs a, int64_t tok_ti
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_mx_gemm<TN>, tw, tx, a, err);
+  return cudaLaunchKernelEx(&cfg, k_mx_gemm<TN, QUANT>, tw, tx, a, err);
 }
 
 }  // namespace
@@ -423,9 +520,18 @@ bool mx_gemm_fits(int64_t M, int64_t N, int64_t groups) {
   return ((M + used * 15) / 16) <= 0x3FFFFFFFLL / n_tiles;
 }
 
-cudaError_t launch_mx_gemm(const MxView& x, const MxView& w, const int32_t* offsets, int groups, int64_t N, void* Y,
-                           int num_sms, int32_t* err, cudaStream_t stream) {
+// Rows of a group that has any: all of them, or their mean over as many groups as can have some.
+static int64_t rows_per_group(int64_t M, int64_t groups) {
+  const int64_t used = groups < M ? groups : M;
+  return used > 0 ? (M + used - 1) / used : 0;
+}
+
+bool mx_gemm_quantizes(int64_t M, int64_t groups) { return rows_per_group(M, groups) <= 16; }
+
+cudaError_t launch_mx_gemm(const MxView& x, const void* x_bf16, const MxView& w, const int32_t* offsets, int groups,
+                           int64_t N, void* Y, int num_sms, int32_t* err, cudaStream_t stream) {
   MxArgs a{};
+  a.x_bf16 = static_cast<const uint4*>(x_bf16);
   a.x_scales = x.scales;
   a.w_scales = w.scales;
   a.offsets = offsets;
@@ -434,15 +540,16 @@ cudaError_t launch_mx_gemm(const MxView& x, const MxView& w, const int32_t* offs
   a.N = N;
   a.w_rows = w.rows;
   a.n_tiles = static_cast<int>((N + kMxRows - 1) / kMxRows);
+  a.K = static_cast<int>(x.cols);
   a.nkb = static_cast<int>((x.cols + kMxBK - 1) / kMxBK);
   a.x_fp4 = x.fmt == kMxE2M1;
   a.Y = static_cast<__nv_bfloat16*>(Y);
-  // rows a group that has any: all of them, or their mean when no fewer groups than rows can be told
-  const int64_t used = offsets ? (groups < a.M ? groups : a.M) : 1;
-  const int64_t per = (a.M + used - 1) / used;
+  const int64_t per = rows_per_group(a.M, groups);
   // most token tiles that any division of the rows into the groups can need
-  auto bound = [&](int tn) { return offsets ? (a.M + used * (tn - 1)) / tn : (a.M + tn - 1) / tn; };
-  if (per <= 16) return run_tiles<16>(x, w, a, bound(16), num_sms, err, stream);
+  const int64_t used = groups < a.M ? groups : a.M;
+  auto bound = [&](int tn) { return (a.M + used * (tn - 1)) / tn; };
+  if (per <= 16) return x_bf16 ? run_tiles<16, true>(x, w, a, bound(16), num_sms, err, stream)
+                               : run_tiles<16>(x, w, a, bound(16), num_sms, err, stream);
   if (per <= 32) return run_tiles<32>(x, w, a, bound(32), num_sms, err, stream);
   if (per <= 64) return run_tiles<64>(x, w, a, bound(64), num_sms, err, stream);
   return run_tiles<128>(x, w, a, bound(128), num_sms, err, stream);

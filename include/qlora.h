@@ -514,6 +514,16 @@ qlora_status qlora_rmsnorm_mx(const void* X, const void* residual, const void* g
 qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y,
                                  qlora_stream_t stream);
 
+/* qlora_mx_linear_fwd_bf16 -- qlora_quantize_mx of bf16 activations X [M, K]
+ * (16-byte aligned) to x_format, then qlora_mx_linear_fwd, in one call with equal
+ * bits. Up to 16 rows are quantized inside the product's kernel, with one launch
+ * and nothing of the workspace used (the size query then returns 256); more rows
+ * are quantized into the workspace first.
+ * Errors: those of the two calls, WORKSPACE. */
+qlora_status qlora_mx_linear_fwd_bf16(const void* X, int64_t M, qlora_mx_format x_format,
+                                      const qlora_mx_tensor* w, void* Y, void* workspace,
+                                      size_t* workspace_bytes, qlora_stream_t stream);
+
 /* qlora_mx_grouped_fwd -- qlora_mx_linear_fwd grouped by expert: rows
  * offsets[e] .. offsets[e + 1] - 1 of x times the transpose of expert e's weight,
  * rows e N .. (e + 1) N - 1 of w, for 0 <= e < n_groups, N = w->rows / n_groups.
@@ -528,6 +538,14 @@ qlora_status qlora_mx_linear_fwd(const qlora_mx_tensor* x, const qlora_mx_tensor
  * The rest as in qlora_mx_linear_fwd. */
 qlora_status qlora_mx_grouped_fwd(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const int32_t* offsets,
                                   int32_t n_groups, void* Y, qlora_stream_t stream);
+
+/* qlora_mx_grouped_fwd_bf16 -- qlora_mx_grouped_fwd of bf16 activations, as
+ * qlora_mx_linear_fwd_bf16 (the workspace is unused where the groups that can have
+ * rows, min(n_groups, M), have 16 or fewer on average). */
+qlora_status qlora_mx_grouped_fwd_bf16(const void* X, int64_t M, qlora_mx_format x_format,
+                                       const qlora_mx_tensor* w, const int32_t* offsets, int32_t n_groups,
+                                       void* Y, void* workspace, size_t* workspace_bytes,
+                                       qlora_stream_t stream);
 
 /* qlora_paged_alloc -- allocate `bytes` of paged memory for optimizer state
  * ([C] 4: a unified pool that pages between GPU and CPU memory, so the state

@@ -133,6 +133,49 @@ def test_refusals_of_the_c_calls():
     assert fwd(none, rw, None, None) == 0 and grp(none, rw, P, 4, None, None) == 0
 
 
+def test_refusals_and_workspace_of_the_quantizing_products():
+    lib = b.load_library()
+    w = _mx(rows=64, fmt=b.MX_E2M1)
+    rw = ctypes.byref(w)
+
+    def size(v=0):
+        return ctypes.byref(ctypes.c_size_t(v))
+
+    def need(M, fmt, groups=None):
+        n = ctypes.c_size_t(0)
+        st = lib.qlora_mx_linear_fwd_bf16(None, M, fmt, rw, None, None, ctypes.byref(n), None) if groups is None else \
+            lib.qlora_mx_grouped_fwd_bf16(None, M, fmt, rw, P, groups, None, None, ctypes.byref(n), None)
+        assert st == 0
+        return n.value
+
+    up = lambda v: (v + 255) // 256 * 256  # noqa: E731
+    assert need(0, b.MX_E4M3) == 256 and need(16, b.MX_E4M3) == 256 and need(64, b.MX_E4M3, groups=4) == 256
+    assert need(17, b.MX_E4M3) == up(17 * 128) + up(17 * 4)
+    assert need(65, b.MX_E2M1, groups=4) == up(65 * 64) + up(65 * 4)
+    lin, grp = lib.qlora_mx_linear_fwd_bf16, lib.qlora_mx_grouped_fwd_bf16
+    big = 1 << 20
+    assert lin(P, 4, 7, rw, P, P, size(big), None) == 2
+    assert lin(P, -1, 0, rw, P, P, size(big), None) == 1
+    assert lin(P, 1 << 31, 0, rw, P, P, size(big), None) == 2
+    assert lin(P, 4, 0, None, P, P, size(big), None) == 1
+    assert lin(P, 4, 0, ctypes.byref(_mx(rows=64)), P, P, size(big), None) == 2
+    assert lin(P, 4, 0, ctypes.byref(_mx(rows=0, fmt=b.MX_E2M1)), P, P, size(big), None) == 1
+    assert lin(None, 4, 0, rw, P, P, size(big), None) == 1
+    assert lin(P, 4, 0, rw, None, P, size(big), None) == 1
+    assert lin(P + 8, 4, 0, rw, P, P, size(big), None) == 3
+    assert lin(P, 4, 0, rw, P + 8, P, size(big), None) == 3
+    assert lin(P, 40, 0, rw, P, P + 128, size(big), None) == 3
+    assert lin(P, 40, 0, rw, P, P, size(100), None) == 5
+    assert lin(P, 40, 0, rw, P, P, None, None) == 1
+    assert lin(None, 0, 0, rw, None, P, size(big), None) == 0
+    assert grp(P, 4, 0, rw, None, 4, P, P, size(big), None) == 1
+    assert grp(P, 4, 0, rw, P, 0, P, P, size(big), None) == 1
+    assert grp(P, 4, 0, rw, P, 4097, P, P, size(big), None) == 2
+    assert grp(P, 4, 0, rw, P + 2, 4, P, P, size(big), None) == 3
+    assert grp(P, 4, 0, rw, P, 5, P, P, size(big), None) == 1
+    assert grp(None, 0, 0, rw, P, 4, None, P, size(big), None) == 0
+
+
 def _tensors(rows, cols, fmt, device="cpu"):
     return b.MXTensor.empty(rows, cols, fmt, device)
 
