@@ -56,6 +56,40 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
   return d;
 }
 
+// One block of 32 bf16 values (two a word) to its codes (8 words of e4m3, 4 of e2m1);
+// returns the scale byte. The maximum is taken on the magnitude bits, two at a time,
+// which order like the values and place NaN above infinity.
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_quantize_block(const uint32_t (&v)[16], uint32_t (&o)[8]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  const uint32_t byte = mx_scale_byte<FMT>(m >> 7);
+  const float inv = mx_inverse_scale(byte);
+  const bool bad = byte == 255u;
+  float f[32];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const f32x2 a = mul_f32x2({bf16lo_to_f32(v[i]), bf16hi_to_f32(v[i])}, {inv, inv});
+    f[2 * i] = a.x;
+    f[2 * i + 1] = a.y;
+  }
+  if (FMT == kMxE4M3) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      o[i] = bad ? 0u : cvt_e4m3x2(f[4 * i], f[4 * i + 1]) | (cvt_e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float g[8] = {f[8 * i],     f[8 * i + 1], f[8 * i + 2], f[8 * i + 3],
+                          f[8 * i + 4], f[8 * i + 5], f[8 * i + 6], f[8 * i + 7]};
+      o[i] = bad ? 0u : cvt_e2m1x8(g);
+    }
+  }
+  return byte;
+}
+
 // Two e4m3 codes (low 16 bits) to two fp32 values (exact).
 __device__ __forceinline__ f32x2 e4m3x2_to_f32x2(uint32_t v) {
   uint32_t h;

@@ -28,23 +28,29 @@ constexpr int kMxBK = 128;     // elements of k a stage
 constexpr int kMxRows = 128;   // weight rows a tile
 constexpr int kMxThreads = 128;   // and four warps more where the kernel quantizes x
 
-template <int TN>
+// Scale words are handled four k-blocks at a time, in a ring of two such blocks: a
+// warp's stores, fence and arrival take some 300 clocks, as long as a k-block's
+// copies and MMAs, so once per k-block they bounded the small products.
+constexpr int kSfDepth = 4;           // k-blocks a block of scales
+constexpr int kSfSlots = 2;
+constexpr int kSfOne = 1024;          // bytes a k-block: words of 128 weight rows, of 128 tokens
+
+template <int TN, bool DEEP>
 struct MxCfg {
   static constexpr int W_BYTES = kMxRows * kMxBK;
   static constexpr int X_BYTES = TN * kMxBK;
-  static constexpr int SF_BYTES = 1024;  // 512 bytes of scale words of the weights, 512 of the tokens
-  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES + SF_BYTES;
-  // Stages when two CTAs share an SM (one streams while the other fills or drains), and when a CTA has it alone: then
-  // nothing but the depth of its ring covers the 2000 clocks from a free slot to its data.
-  static constexpr int STAGES = (110 * 1024 - 1536) / STAGE_BYTES;
-  static constexpr int DEEP = (220 * 1024 - 1536) / STAGE_BYTES;
-  static constexpr int SF_COL = TN < 32 ? 32 : TN;  // first TMEM column of the scales
-  static constexpr int TMEM_NEED = SF_COL + 8 * DEEP;
-  static constexpr int TMEM_COLS = TMEM_NEED <= 64 ? 64 : (TMEM_NEED <= 128 ? 128 : 256);
-  static constexpr int smem(int stages) { return stages * STAGE_BYTES + 1024 /*align*/ + 256 /*barriers*/; }
-  static_assert(16 * DEEP + 16 <= 256, "barriers");
+  static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
+  static constexpr int SF_BYTES = kSfSlots * kSfDepth * kSfOne;
+  // The ring's round trip (a k-block's MMAs done, slot free, copy issued, data there) takes 1500 to 2000 clocks. With
+  // two CTAs on an SM one streams while the other waits; DEEP is for grids that leave a CTA alone on its SM.
+  static constexpr int ROOM = (DEEP ? 220 : 110) * 1024 - 1536 - SF_BYTES;
+  static constexpr int STAGES = ROOM / STAGE_BYTES < kSfSlots * kSfDepth ? ROOM / STAGE_BYTES : kSfSlots * kSfDepth;
+  static constexpr int SF_COL = TN < 32 ? 32 : TN;  // first TMEM column of the scales, 8 a k-block
+  static constexpr int TMEM_NEED = SF_COL + 8 * kSfSlots * kSfDepth;
+  static constexpr int TMEM_COLS = TMEM_NEED <= 128 ? 128 : 256;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + SF_BYTES + 1024 /*align*/ + 256 /*barriers*/;
   static_assert(STAGES * STAGE_BYTES >= TN * kMxRows * 4, "the partial tile reuses the stages");
-  static_assert(TMEM_COLS >= 64, "the epilogue reads 64 columns at a time");
+  static_assert(STAGES <= kSfSlots * kSfDepth, "a free stage has to mean free scales");
 };
 
 // Instruction descriptor of kind::mxf8f6f4.block_scale (fp32 accumulator, ue8m0
@@ -268,86 +274,76 @@ struct MxArgs {
   int groups;
   int64_t M, N, w_rows;
   int n_tiles, nkb, K;
-  int stages, stage_bytes;  // the ring (its stages' size is only the pairs' to choose)
+  int stages, stage_bytes;  // pairs: the operands' ring
   int tn, step, tok_tiles;  // pairs: most tokens a tile; without groups, tokens of all tiles but the last and their count
   uint32_t idesc;
   bool x_fp4;  // the widening copies of e2m1 count the bytes of codes, not of containers
   __nv_bfloat16* Y;
 };
 
-// The tokens' side of the stages, from bf16 (warps 4..7 of the QUANT kernel).
-template <int TN, int FMT>
+// The tokens' side of the stages, from bf16 (warps 4..7 of the QUANT kernel): warp q
+// writes every fourth k-block, lane l the 64 elements (two MX blocks) of half l % 2 of
+// token l / 2, one k-block of its own ahead in registers. The scale words go to the
+// k-block's place in the scales' ring, which is free when the stage is (the ring of
+// scales holds more k-blocks than the ring of stages).
+template <int TN, bool DEEP, int FMT>
 __device__ __forceinline__ void quantize_stages(const MxArgs& a, int64_t row0, int tokens, int kb0, int kb1,
-                                                uint8_t* smem, uint64_t* full, uint64_t* empty,
+                                                uint8_t* smem, uint8_t* sf, uint64_t* full, uint64_t* empty,
                                                 volatile int* abort_flag, int32_t* err) {
-  using C = MxCfg<TN>;
-  static_assert(TN * 8 == 128, "a thread holds 16 elements of a stage");
-  constexpr int AHEAD = 4;
-  const int t = threadIdx.x - kMxThreads;
-  const int row = t >> 3, h = t & 7;  // token, and which 16 of the stage's 128 elements
+  using C = MxCfg<TN, DEEP>;
+  static_assert(TN == 16, "a lane holds half a token's k-block");
+  const int lane = threadIdx.x & 31;
+  const int row = lane >> 1, h = lane & 1;
   const bool mine = row < tokens;
-  const uint4* src = a.x_bf16 + ((row0 + (mine ? row : 0)) * a.K + h * 16) / 8;
-  uint4 q[AHEAD][2];
-  auto load = [&](int kb, uint4 (&d)[2]) {
-    d[0] = d[1] = make_uint4(0u, 0u, 0u, 0u);
-    if (mine && kb < kb1 && kb * kMxBK + h * 16 < a.K) {
-      d[0] = __ldg(src + kb * (kMxBK / 8));
-      d[1] = __ldg(src + kb * (kMxBK / 8) + 1);
+  const uint4* src = a.x_bf16 + ((row0 + (mine ? row : 0)) * a.K + h * 64) / 8;
+  uint4 q[8];
+  auto load = [&](int kb) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      q[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (mine && kb < kb1 && kb * kMxBK + h * 64 + (i >> 2) * 32 < a.K) q[i] = __ldg(src + kb * (kMxBK / 8) + i);
     }
   };
+  const int first = kb0 + (threadIdx.x >> 5) - kMxThreads / 32;
+  load(first);
+  for (int kb = first; kb < kb1; kb += 4) {
+    const int n = kb - kb0, stage = n % C::STAGES;
+    const uint32_t phase = (n / C::STAGES) & 1;
+    uint32_t o[2][8];
+    uint32_t bytes = 0;
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) load(kb0 + i, q[i]);
-  int stage = 0;
-  uint32_t phase = 0;
-  for (int base = kb0; base < kb1; base += AHEAD) {
+    for (int b = 0; b < 2; ++b) {
+      uint32_t v[16];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int kb = base + i;
-      if (kb >= kb1) return;
-      const uint32_t v[8] = {q[i][0].x, q[i][0].y, q[i][0].z, q[i][0].w, q[i][1].x, q[i][1].y, q[i][1].z, q[i][1].w};
-      load(kb + AHEAD, q[i]);
-      uint32_t m = 0u;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = __vmaxu2(m, v[j] & 0x7FFF7FFFu);
-      m = max(m & 0xFFFFu, m >> 16);
-      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));  // the block's other half
-      const uint32_t byte = mx_scale_byte<FMT>(m >> 7);
-      const float inv = mx_inverse_scale(byte);
-      float f[16];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const f32x2 p = mul_f32x2({bf16lo_to_f32(v[j]), bf16hi_to_f32(v[j])}, {inv, inv});
-        f[2 * j] = p.x;
-        f[2 * j + 1] = p.y;
+      for (int i = 0; i < 4; ++i) {
+        v[4 * i] = q[4 * b + i].x;
+        v[4 * i + 1] = q[4 * b + i].y;
+        v[4 * i + 2] = q[4 * b + i].z;
+        v[4 * i + 3] = q[4 * b + i].w;
       }
-      const bool bad = byte == 255u;
-      if (!__all_sync(0xffffffffu, wait_or_abort(&empty[stage], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY)))
-        return;
-      uint8_t* sx = smem + stage * C::STAGE_BYTES + C::W_BYTES;
-      if (mine) {
-        uint8_t* dst = sx + row * 128 + ((h ^ (row & 7)) << 4);  // 128-byte swizzle
-        if (FMT == kMxE4M3) {
-          uint4 o;
-          o.x = cvt_e4m3x2(f[0], f[1]) | (cvt_e4m3x2(f[2], f[3]) << 16);
-          o.y = cvt_e4m3x2(f[4], f[5]) | (cvt_e4m3x2(f[6], f[7]) << 16);
-          o.z = cvt_e4m3x2(f[8], f[9]) | (cvt_e4m3x2(f[10], f[11]) << 16);
-          o.w = cvt_e4m3x2(f[12], f[13]) | (cvt_e4m3x2(f[14], f[15]) << 16);
-          *reinterpret_cast<uint4*>(dst) = bad ? make_uint4(0u, 0u, 0u, 0u) : o;
-        } else {
-          const float lo[8] = {f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]};
-          const float hi[8] = {f[8], f[9], f[10], f[11], f[12], f[13], f[14], f[15]};
-          *reinterpret_cast<uint2*>(dst) = bad ? make_uint2(0u, 0u) : make_uint2(cvt_e2m1x8(lo), cvt_e2m1x8(hi));
-        }
-        if ((h & 1) == 0) sx[C::X_BYTES + 512 + row * 16 + (h >> 1)] = static_cast<uint8_t>(byte);
-      }
-      fence_async_shared();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(&full[stage]);
-      if (++stage == a.stages) {
-        stage = 0;
-        phase ^= 1u;
-      }
+      bytes |= mx_quantize_block<FMT>(v, o[b]) << (8 * b);
     }
+    load(kb + 4);
+    if (!__all_sync(0xffffffffu, wait_or_abort(&empty[stage], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY)))
+      return;
+    if (mine) {
+      uint8_t* line = smem + stage * C::STAGE_BYTES + C::W_BYTES + row * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {  // 16 elements: a 16-byte piece of the row, at its place in the 128-byte swizzle
+        uint8_t* dst = line + (((h * 4 + c) ^ (row & 7)) << 4);
+        const uint32_t(&p)[8] = o[c >> 1];
+        if (FMT == kMxE4M3)
+          *reinterpret_cast<uint4*>(dst) =
+              make_uint4(p[4 * (c & 1)], p[4 * (c & 1) + 1], p[4 * (c & 1) + 2], p[4 * (c & 1) + 3]);
+        else  // 8 bytes of codes, 8 unused
+          *reinterpret_cast<uint2*>(dst) = make_uint2(p[2 * (c & 1)], p[2 * (c & 1) + 1]);
+      }
+      *reinterpret_cast<uint16_t*>(sf + (n % (kSfSlots * kSfDepth)) * kSfOne + 512 + row * 16 + h * 2) =
+          static_cast<uint16_t>(bytes);
+    }
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&full[stage]);
   }
 }
 
@@ -357,21 +353,22 @@ __device__ __forceinline__ void quantize_stages(const MxArgs& a, int64_t row0, i
 // accumulator. With S > 1 each CTA leaves its fp32 partial in shared memory and
 // adds up its share of the tokens over the cluster, in the order of the CTAs.
 //
-// QUANT (TN = 16): x is bf16, and four more warps write the tokens' side of a stage
-// themselves: thread t holds 16 elements, half an MX block, of token t / 8, four
-// stages ahead in registers, so that a decode step is one launch and its
-// activations are never stored. A few tokens are quantized again by every CTA,
+// QUANT (TN = 16): x is bf16, and four more warps write the tokens' side of the stages
+// themselves, so that a decode step is one launch and its activations are never stored. A few tokens are quantized again by every CTA,
 // which costs less than a launch and a round trip through memory.
-template <int TN, bool QUANT>
+template <int TN, bool QUANT, bool DEEP>
 __global__ void __launch_bounds__(QUANT ? kMxThreads + 128 : kMxThreads)
 k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const MxArgs a,
           int32_t* err) {
-  using C = MxCfg<TN>;
+  using C = MxCfg<TN, DEEP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + a.stages * C::STAGE_BYTES);
-  uint64_t* empty = full + a.stages;
-  uint64_t* accf = empty + a.stages;
+  uint8_t* sf = smem + C::STAGES * C::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sf + C::SF_BYTES);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* sf_full = empty + C::STAGES;
+  uint64_t* sf_empty = sf_full + kSfSlots;
+  uint64_t* accf = sf_empty + kSfSlots;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(accf + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -382,9 +379,13 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
   const uint32_t rank = S > 1 ? cluster_ctarank() : 0u;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.stages; ++s) {
-      mbar_init(&full[s], QUANT ? 6 : 3);  // the TMA warp, the scale warp(s), the four quantizing warps
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], QUANT ? 2 : 1);  // the TMA warp, the warp that quantizes the stage
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < kSfSlots; ++s) {
+      mbar_init(&sf_full[s], QUANT ? 1 : 2);  // the scale warps
+      mbar_init(&sf_empty[s], 1);
     }
     mbar_init(accf, 1);
     *abort_flag = 0;
@@ -417,57 +418,82 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     if (warp == 0) {
       const uint32_t bytes = C::W_BYTES / 2 + (QUANT ? 0 : a.x_fp4 ? C::X_BYTES / 2 : C::X_BYTES);
       const int32_t wrow = static_cast<int32_t>(w0), xrow = static_cast<int32_t>(tt.row0);
-      int stage = 0, issued = 0;
-      uint32_t phase = 0;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!__all_sync(0xffffffffu,
-                        wait_or_abort(&empty[stage], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY)))
-          break;
-        if (elect_one()) {
-          uint8_t* sw = smem + stage * C::STAGE_BYTES;
-          mbar_arrive_expect_tx(&full[stage], bytes);
-          tma_load_2d(sw, &tm_w, &full[stage], kb * kMxBK, wrow);
-          if (!QUANT) tma_load_2d(sw + C::W_BYTES, &tm_x, &full[stage], kb * kMxBK, xrow);
+      if (elect_one()) {
+        bool ok = true;
+        int issued = 0;
+        for (int round = 0, kb = kb0; kb < kb1 && ok; ++round) {
+#pragma unroll
+          for (int st = 0; st < C::STAGES; ++st, ++kb) {
+            if (kb < kb1 && ok) {
+              if (round > 0)
+                ok = wait_or_abort(&empty[st], (round - 1) & 1, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY);
+              if (ok) {
+                uint8_t* sw = smem + st * C::STAGE_BYTES;
+                mbar_arrive_expect_tx(&full[st], bytes);
+                tma_load_2d(sw, &tm_w, &full[st], kb * kMxBK, wrow);
+                if (!QUANT) tma_load_2d(sw + C::W_BYTES, &tm_x, &full[st], kb * kMxBK, xrow);
+                ++issued;
+              }
+            }
+          }
         }
-        __syncwarp();
-        ++issued;
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        // after an abort, let the copies already issued land before the CTA leaves
+        if (*abort_flag)
+          for (int i = max(0, issued - C::STAGES); i < issued; ++i)
+            mbar_wait_bounded(&full[i % C::STAGES], (i / C::STAGES) & 1, err, DEV_TIMEOUT_TMA_FULL);
       }
-      // after an abort, let the copies already issued land before the CTA leaves
-      if (*abort_flag && lane == 0)
-        for (int i = max(0, issued - a.stages); i < issued; ++i)
-          mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, err, DEV_TIMEOUT_TMA_FULL);
     } else if (warp == 1) {
       const uint32_t s0 = smem_u32(smem);
       const uint64_t dw0 = smem_desc(s0, 16, 1024), dx0 = smem_desc(s0 + C::W_BYTES, 16, 1024);
-      const uint64_t df0 = smem_desc_scales(s0 + C::W_BYTES + C::X_BYTES);
-      int stage = 0;
-      uint32_t phase = 0;
+      const uint64_t df0 = smem_desc_scales(smem_u32(sf));
+      int stage = 0, slot = 0;
+      uint32_t phase = 0, sf_phase = 0;
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        ok = __all_sync(0xffffffffu, wait_or_abort(&full[stage], phase, abort_flag, err, DEV_TIMEOUT_TMA_FULL));
+      for (int base = kb0; base < kb1; base += kSfDepth) {
+        ok = __all_sync(0xffffffffu, wait_or_abort(&sf_full[slot], sf_phase, abort_flag, err, DEV_TIMEOUT_TMA_FULL));
         if (!ok) break;
-        tc_fence_after();
-        const uint64_t at = static_cast<uint64_t>(stage) * (C::STAGE_BYTES >> 4);  // in descriptors' 16-byte units
-        // the stage's own TMEM columns: the MMAs that read them last have
-        // completed, or the stage would not have been refilled
-        const uint32_t tsf = tmem_base + C::SF_COL + 8u * stage;
-        if (elect_one()) {
-          tmem_copy_scales(tsf, df0 + at);
-          tmem_copy_scales(tsf + 4, df0 + at + (512 >> 4));
+        int st[kSfDepth];
+        uint32_t ph[kSfDepth];
 #pragma unroll
-          for (uint32_t j = 0; j < kMxBK / 32; ++j)
-            mma_mx(tmem_base, dw0 + at + j * 2, dx0 + at + j * 2, a.idesc | (j << 4) | (j << 29), tsf, tsf + 4,
-                   (kb > kb0 || j > 0) ? 1u : 0u);
-          mma_commit(&empty[stage]);
+        for (int i = 0; i < kSfDepth; ++i) {
+          st[i] = stage;
+          ph[i] = phase;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (elect_one()) {
+          bool good = true;
+#pragma unroll
+          for (int i = 0; i < kSfDepth; ++i) {
+            if (base + i < kb1 && good) {
+              good = wait_or_abort(&full[st[i]], ph[i], abort_flag, err, DEV_TIMEOUT_TMA_FULL);
+              if (good) {
+                tc_fence_after();
+                const uint64_t at = static_cast<uint32_t>(st[i] * C::STAGE_BYTES) >> 4;  // 16-byte units, as descriptors
+                const uint64_t df = df0 + ((slot * kSfDepth + i) * (kSfOne >> 4));
+                // TMEM columns of the k-block's own place: the MMAs that read them last have completed, or the scales
+                // would not have been refilled
+                const uint32_t tsf = tmem_base + C::SF_COL + 8 * (slot * kSfDepth + i);
+                tmem_copy_scales(tsf, df);
+                tmem_copy_scales(tsf + 4, df + (512 >> 4));
+#pragma unroll
+                for (uint32_t j = 0; j < kMxBK / 32; ++j)
+                  mma_mx(tmem_base, dw0 + at + j * 2, dx0 + at + j * 2, a.idesc | (j << 4) | (j << 29), tsf, tsf + 4,
+                         (base + i > kb0 || j > 0) ? 1u : 0u);
+                mma_commit(&empty[st[i]]);
+              }
+            }
+          }
+          if (good) mma_commit(&sf_empty[slot]);
         }
         __syncwarp();
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1u;
+        ok = __all_sync(0xffffffffu, *abort_flag == 0);
+        if (!ok) break;
+        if (++slot == kSfSlots) {
+          slot = 0;
+          sf_phase ^= 1u;
         }
       }
       if (ok && elect_one()) mma_commit(accf);
@@ -475,41 +501,35 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
       if constexpr (QUANT) {
         const int tokens = static_cast<int>(min(static_cast<int64_t>(TN), tt.end - tt.row0));
         if (a.x_fp4)
-          quantize_stages<TN, kMxE2M1>(a, tt.row0, tokens, kb0, kb1, smem, full, empty, abort_flag, err);
+          quantize_stages<TN, DEEP, kMxE2M1>(a, tt.row0, tokens, kb0, kb1, smem, sf, full, empty, abort_flag, err);
         else
-          quantize_stages<TN, kMxE4M3>(a, tt.row0, tokens, kb0, kb1, smem, full, empty, abort_flag, err);
+          quantize_stages<TN, DEEP, kMxE4M3>(a, tt.row0, tokens, kb0, kb1, smem, sf, full, empty, abort_flag, err);
       }
     } else if (!QUANT || warp == 2) {
       // scale words of 128 weight rows (warp 2) or TN tokens (warp 3)
-      constexpr int AHEAD = 4;
       const bool wside = warp == 2;
-      ScaleWords<1, AHEAD> sc;
+      ScaleWords<1, kSfDepth> sc;
       if (wside)
         sc.start(a.w_scales, a.w_rows, w0, kMxRows, kb0, kb1);
       else
         sc.start(a.x_scales, a.M, tt.row0, TN, kb0, kb1);
-      uint8_t* dst = smem + C::W_BYTES + C::X_BYTES + (wside ? 0 : 512);
-      int stage = 0;
+      uint8_t* dst = sf + (wside ? 0 : 512);
+      int slot = 0;
       uint32_t phase = 0;
-      bool ok = true;
-      for (int base = kb0; base < kb1 && ok; base += AHEAD) {
+      for (int base = kb0; base < kb1; base += kSfDepth) {
+        if (!__all_sync(0xffffffffu,
+                        wait_or_abort(&sf_empty[slot], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY)))
+          break;
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          if (base + i < kb1 && ok) {
-            ok = __all_sync(0xffffffffu,
-                            wait_or_abort(&empty[stage], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY));
-            if (ok) {
-              sc.store(i, dst + stage * C::STAGE_BYTES);
-              sc.load(i, base + i + AHEAD, kb1);
-              fence_async_shared();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&full[stage]);
-              if (++stage == a.stages) {
-                stage = 0;
-                phase ^= 1u;
-              }
-            }
-          }
+        for (int i = 0; i < kSfDepth; ++i) sc.store(i, dst + (slot * kSfDepth + i) * kSfOne);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sf_full[slot]);
+#pragma unroll
+        for (int i = 0; i < kSfDepth; ++i) sc.load(i, base + kSfDepth + i, kb1);
+        if (++slot == kSfSlots) {
+          slot = 0;
+          phase ^= 1u;
         }
       }
     }
@@ -811,14 +831,15 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       const int32_t wrow = static_cast<int32_t>(t.w0 + rank * 128);
       const int32_t xrow = static_cast<int32_t>(t.row0 + rank * half);
       const uint32_t bytes = 2 * (kPairW / 2 + half * (a.x_fp4 ? kMxBK / 2 : kMxBK));
-      for (int kb = 0; kb < a.nkb; ++kb) {
-        ok = __all_sync(0xffffffffu,
-                        wait_or_abort(&empty[stage], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY));
-        if (!ok) break;
-        if (elect_one()) {
-          uint8_t* sw = smem + stage * a.stage_bytes;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
-          const uint32_t fbar = fbar0 + stage * 8;
+      if (elect_one()) {
+        int st = stage;
+        uint32_t ph = phase;
+        for (int kb = 0; kb < a.nkb && ok; ++kb) {
+          ok = wait_or_abort(&empty[st], ph ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY);
+          if (!ok) break;
+          uint8_t* sw = smem + st * a.stage_bytes;
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
+          const uint32_t fbar = fbar0 + st * 8;
           tma_load_2d_pair(sw, &tm_w, fbar, kb * kMxBK, wrow);
           int at = 0;
 #pragma unroll
@@ -828,14 +849,18 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
               at += 128 >> b;
             }
           }
-        }
-        __syncwarp();
-        ++issued;
-        if (++stage == a.stages) {
-          stage = 0;
-          phase ^= 1u;
+          if (++st == a.stages) {
+            st = 0;
+            ph ^= 1u;
+          }
         }
       }
+      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok);
+      issued += a.nkb;  // (after an abort the waits below just run out)
+      const int turns = (stage + a.nkb) / a.stages;
+      stage = stage + a.nkb - turns * a.stages;
+      phase ^= turns & 1;
     }
     // after an abort, let the copies already issued land before the pair leaves
     if (lane == 0 && rank == 0 && *abort_flag)
@@ -863,34 +888,47 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         for (int base = 0; base < a.nkb && ok; base += kPairSfDepth) {
           ok = __all_sync(0xffffffffu,
                           wait_or_abort_cluster(&sf_full[slot], sf_phase, abort_flag, err, DEV_TIMEOUT_TMA_FULL));
-          const int end = min(a.nkb, base + kPairSfDepth);
-          for (int kb = base; kb < end && ok; ++kb) {
-            ok = __all_sync(0xffffffffu, wait_or_abort(&full[stage], phase, abort_flag, err, DEV_TIMEOUT_TMA_FULL));
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t at = static_cast<uint32_t>(stage * a.stage_bytes) >> 4;
-            const uint32_t one = slot * kPairSfDepth + (kb - base);  // this k-block's place among the scales
-            const uint64_t df = df0 + static_cast<uint64_t>(one) * (kPairSfOne >> 4);
-            // TMEM columns of its own: the MMAs that read them last have completed, or the slot would not have been
-            // refilled
-            const uint32_t tsf = tmem_base + kPairSfCol + kPairSfCols * one;
-            if (elect_one()) {
-              tmem_copy_scales_pair(tsf, df);
-              tmem_copy_scales_pair(tsf + 4, df + (512 >> 4));
-              if (wide) tmem_copy_scales_pair(tsf + 8, df + (1024 >> 4));
+          if (!ok) break;
+          int st[kPairSfDepth];
+          uint32_t ph[kPairSfDepth];
 #pragma unroll
-              for (uint32_t j = 0; j < kMxBK / 32; ++j)
-                mma_mx_pair(tmem_base, dw0 + at + j * 2, dx0 + at + j * 2, idesc | (j << 4) | (j << 29), tsf, tsf + 4,
-                            (kb > 0 || j > 0) ? 1u : 0u);
-              mma_commit_pair(&empty[stage]);
-              if (kb + 1 == end) mma_commit_pair(&sf_empty[slot]);
-            }
-            __syncwarp();
-            if (++stage == a.stages) {
+          for (int i = 0; i < kPairSfDepth; ++i) {
+            st[i] = stage;
+            ph[i] = phase;
+            if (base + i < a.nkb && ++stage == a.stages) {
               stage = 0;
               phase ^= 1u;
             }
           }
+          if (elect_one()) {
+            bool good = true;
+#pragma unroll
+            for (int i = 0; i < kPairSfDepth; ++i) {
+              if (base + i < a.nkb && good) {
+                good = wait_or_abort(&full[st[i]], ph[i], abort_flag, err, DEV_TIMEOUT_TMA_FULL);
+                if (good) {
+                  tc_fence_after();
+                  const uint64_t at = static_cast<uint32_t>(st[i] * a.stage_bytes) >> 4;
+                  const uint32_t one = slot * kPairSfDepth + i;  // this k-block's place among the scales
+                  const uint64_t df = df0 + one * (kPairSfOne >> 4);
+                  // TMEM columns of its own: the MMAs that read them last have completed, or the slot would not have
+                  // been refilled
+                  const uint32_t tsf = tmem_base + kPairSfCol + kPairSfCols * one;
+                  tmem_copy_scales_pair(tsf, df);
+                  tmem_copy_scales_pair(tsf + 4, df + (512 >> 4));
+                  if (wide) tmem_copy_scales_pair(tsf + 8, df + (1024 >> 4));
+#pragma unroll
+                  for (uint32_t j = 0; j < kMxBK / 32; ++j)
+                    mma_mx_pair(tmem_base, dw0 + at + j * 2, dx0 + at + j * 2, idesc | (j << 4) | (j << 29), tsf,
+                                tsf + 4, (base + i > 0 || j > 0) ? 1u : 0u);
+                  mma_commit_pair(&empty[st[i]]);
+                }
+              }
+            }
+            if (good) mma_commit_pair(&sf_empty[slot]);
+          }
+          __syncwarp();
+          ok = __all_sync(0xffffffffu, *abort_flag == 0);
           if (++slot == kPairSfSlots) {
             slot = 0;
             sf_phase ^= 1u;
@@ -973,29 +1011,16 @@ bool make_mx_map(CUtensorMap* m, const MxView& v, int box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TN, bool QUANT = false>
-cudaError_t run_tiles(const MxView& x, const MxView& w, MxArgs a, int64_t tok_tiles, int num_sms, int32_t* err,
-                      cudaStream_t stream) {
-  using C = MxCfg<TN>;
-  CUtensorMap tw, tx;
-  if (!make_mx_map(&tw, w, kMxRows)) return cudaErrorInvalidValue;
-  if (QUANT)
-    tx = tw;  // not used
-  else if (!make_mx_map(&tx, x, TN))
-    return cudaErrorInvalidValue;
-  a.idesc = mx_instr_desc(kFmtE2M1, x.fmt == kMxE2M1 ? kFmtE2M1 : kFmtE4M3, kMxRows, TN);
-  const int64_t tiles = tok_tiles * a.n_tiles;
-  // CTAs a tile: as many as are on the card at once, with at least 4 stages of work each
-  int S = static_cast<int>(2 * num_sms / tiles < 8 ? 2 * num_sms / tiles : 8);
-  if (S > a.nkb / 4) S = a.nkb / 4;
-  if (S < 1) S = 1;
-  a.stages = tiles * S <= num_sms ? C::DEEP : C::STAGES;
-  const cudaError_t e = ensure_smem_limit<k_mx_gemm<TN, QUANT>>(C::smem(C::DEEP));
+template <int TN, bool QUANT, bool DEEP>
+cudaError_t launch_tiles(const CUtensorMap& tw, const CUtensorMap& tx, const MxArgs& a, int64_t tiles, int S,
+                         int32_t* err, cudaStream_t stream) {
+  using C = MxCfg<TN, DEEP>;
+  const cudaError_t e = ensure_smem_limit<k_mx_gemm<TN, QUANT, DEEP>>(C::SMEM);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
   cfg.blockDim = dim3(QUANT ? kMxThreads + 128 : kMxThreads);
-  cfg.dynamicSmemBytes = C::smem(a.stages);
+  cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1006,7 +1031,30 @@ cudaError_t run_tiles(const MxView& x, const MxView& w, MxArgs a, int64_t tok_ti
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_mx_gemm<TN, QUANT>, tw, tx, a, err);
+  return cudaLaunchKernelEx(&cfg, k_mx_gemm<TN, QUANT, DEEP>, tw, tx, a, err);
+}
+
+template <int TN, bool QUANT = false>
+cudaError_t run_tiles(const MxView& x, const MxView& w, MxArgs a, int64_t tok_tiles, int num_sms, int32_t* err,
+                      cudaStream_t stream) {
+  CUtensorMap tw, tx;
+  if (!make_mx_map(&tw, w, kMxRows)) return cudaErrorInvalidValue;
+  if (QUANT)
+    tx = tw;  // not used
+  else if (!make_mx_map(&tx, x, TN))
+    return cudaErrorInvalidValue;
+  a.idesc = mx_instr_desc(kFmtE2M1, x.fmt == kMxE2M1 ? kFmtE2M1 : kFmtE4M3, kMxRows, TN);
+  const int64_t tiles = tok_tiles * a.n_tiles;
+  // CTAs a tile: one on each SM (one token, 4096x4096: 5.9 us with 4 a tile, 6.3 with 8, two to an SM), or where that
+  // leaves SMs without one, two on each (11008x4096: 7.3 us with 3 a tile, 8.6 with 1; not with 128 tokens, whose partial
+  // tiles cost more to add up: 13.9 and 12.1); each with at least 4 k-blocks.
+  int64_t most = num_sms / tiles;
+  if (most == 1 && TN <= 64) most = 2 * num_sms / tiles;
+  if (most > 8) most = 8;
+  if (most > a.nkb / 4) most = a.nkb / 4;
+  const int S = most < 1 ? 1 : static_cast<int>(most);
+  if (tiles * S <= num_sms) return launch_tiles<TN, QUANT, true>(tw, tx, a, tiles, S, err, stream);
+  return launch_tiles<TN, QUANT, false>(tw, tx, a, tiles, S, err, stream);
 }
 
 // tn: most tokens a tile, a multiple of 32 up to 256.
@@ -1073,10 +1121,10 @@ cudaError_t launch_mx_gemm(const MxView& x, const void* x_bf16, const MxView& w,
   if (per <= 16) return x_bf16 ? run_tiles<16, true>(x, w, a, bound(16), num_sms, err, stream)
                                : run_tiles<16>(x, w, a, bound(16), num_sms, err, stream);
   if (per <= 32) return run_tiles<32>(x, w, a, bound(32), num_sms, err, stream);
-  if (per <= 64) return run_tiles<64>(x, w, a, bound(64), num_sms, err, stream);
-  // One CTA a tile of 128 tokens while every tile has an SM (333 tokens, 4096x4096: 12.7 us against 15.0 in pairs; 512:
-  // 13.2 against 15.8); pairs beyond that, where the traffic of the smaller tiles counts (512 tokens, 11008x4096: 35.1
-  // against 27.0).
+  // The narrowest tile that still gives every tile an SM (200 tokens, 4096x4096: 9.6 us in tiles of 64, 10.7 of 128; 333:
+  // 13.0 and 11.7), then pairs, whose tiles read less (1024 tokens, 4096x4096: 19.0 us, 18.6 in 256 tiles of 128 tokens;
+  // 512, 11008x4096: 27.0 and 33.1).
+  if (per <= 64 || bound(64) * a.n_tiles <= num_sms) return run_tiles<64>(x, w, a, bound(64), num_sms, err, stream);
   if (bound(128) * a.n_tiles <= num_sms) return run_tiles<128>(x, w, a, bound(128), num_sms, err, stream);
   // Tokens a tile: a k-block takes 2 clocks a token, but not under 440 (the copies' round trip); the last round of tiles
   // is as long as the others. Groups come in all sizes, and their tiles shrink to fit: the widest.

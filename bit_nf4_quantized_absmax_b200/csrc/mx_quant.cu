@@ -41,9 +41,7 @@ __device__ __forceinline__ uint32_t gather_scale_word(uint32_t byte) {
 }
 
 // One thread quantizes one block of 32: 64 contiguous bytes in, 32 (e4m3) or 16
-// (e2m1) out, no exchange between threads but the scale word's. The block
-// maximum is taken on the magnitude bits, two at a time, which order like the
-// values and place NaN above infinity.
+// (e2m1) out, no exchange between threads but the scale word's.
 template <int FMT, bool V8>
 __global__ void __launch_bounds__(kQuantThreads)
 k_mx_quantize(const uint4* __restrict__ X, int64_t rows, int cols, uint8_t* __restrict__ data,
@@ -86,40 +84,17 @@ k_mx_quantize(const uint4* __restrict__ X, int64_t rows, int cols, uint8_t* __re
         }
       }
     }
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = __vmaxu2(m, v[i] & 0x7FFF7FFFu);
-    m = max(m & 0xFFFFu, m >> 16);
-    const uint32_t byte = valid ? mx_scale_byte<FMT>(m >> 7) : 127u;
+    uint32_t o[8];
+    uint32_t byte = mx_quantize_block<FMT>(v, o);
+    if (!valid) byte = 127u;  // the padding; its codes are 0
     const uint32_t word = gather_scale_word(byte);
     if (in && (threadIdx.x & 3) == 0) scales[static_cast<int64_t>(kb >> 2) * rows + row] = word;
     if (!in) continue;
-    const bool bad = byte == 255u;
-    const float inv = mx_inverse_scale(byte);
     if (FMT == kMxE4M3) {
-      uint32_t o[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const f32x2 a = mul_f32x2({bf16lo_to_f32(v[2 * i]), bf16hi_to_f32(v[2 * i])}, {inv, inv});
-        const f32x2 b = mul_f32x2({bf16lo_to_f32(v[2 * i + 1]), bf16hi_to_f32(v[2 * i + 1])}, {inv, inv});
-        o[i] = bad ? 0u : cvt_e4m3x2(a.x, a.y) | (cvt_e4m3x2(b.x, b.y) << 16);
-      }
       uint4* dst = reinterpret_cast<uint4*>(data + row * kp + kb * 32);
       dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
       dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     } else {
-      uint32_t o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f32x2 a = mul_f32x2({bf16lo_to_f32(v[4 * i + j]), bf16hi_to_f32(v[4 * i + j])}, {inv, inv});
-          f[2 * j] = a.x;
-          f[2 * j + 1] = a.y;
-        }
-        o[i] = bad ? 0u : cvt_e2m1x8(f);
-      }
       *reinterpret_cast<uint4*>(data + (row * kp + kb * 32) / 2) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
