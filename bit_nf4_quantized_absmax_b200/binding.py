@@ -8,7 +8,6 @@ not been built; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from dataclasses import dataclass
 
@@ -468,9 +467,11 @@ def qlora_merge_lora(q: NF4Weight | SingleNF4Weight, adapters, out: torch.Tensor
 
 MX_E4M3, MX_E2M1 = 0, 1
 
-# The current stream's handle without a Stream object (0.1 against 3 us a call, of about 10).
+# The MX calls are also made for single tokens, where the host's part is as long as the kernel: the current stream's
+# handle is taken without a Stream object (0.1 against 3 us), and checks are plain comparisons.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_BF16, _U8 = torch.bfloat16, torch.uint8
 
 
 def _require(ok: bool, what: str):
@@ -480,12 +481,14 @@ def _require(ok: bool, what: str):
 
 def _mx_bytes(rows: int, cols: int, format: int) -> tuple:
     """Bytes of data and scales (qlora_mx_storage_bytes, without a call)."""
-    if not (format == MX_E4M3 or format == MX_E2M1):
-        raise ValueError(f"unknown MX format {format!r}")
     if cols <= 0 or cols % 32 or rows < 0:
         raise ValueError(f"MX storage needs cols % 32 == 0, got [{rows}, {cols}]")
     kp = (cols + 127) // 128 * 128
-    return rows * (kp // 2 if format == MX_E2M1 else kp), rows * (kp // 32)
+    if format == MX_E2M1:
+        return rows * (kp >> 1), rows * (kp >> 5)
+    if format == MX_E4M3:
+        return rows * kp, rows * (kp >> 5)
+    raise ValueError(f"unknown MX format {format!r}")
 
 
 class MXTensor:
@@ -497,14 +500,14 @@ class MXTensor:
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, format: int):
         nd, ns = _mx_bytes(rows, cols, format)
-        _require(data.dtype == torch.uint8 and scales.dtype == torch.uint8 and data.is_contiguous()
-                 and scales.is_contiguous() and data.device == scales.device,
-                 "MX data and scales are contiguous uint8 tensors of one device")
+        device = data.device
+        if data.dtype != _U8 or scales.dtype != _U8 or scales.device != device or not data.is_contiguous() or \
+                not scales.is_contiguous():
+            raise ValueError("MX data and scales are contiguous uint8 tensors of one device")
         if data.numel() != nd or scales.numel() != ns:
             raise ValueError(f"data and scales of {data.numel()} and {scales.numel()} bytes do not hold "
                              f"[{rows}, {cols}] ({nd} and {ns} bytes)")
-        self._data, self._scales, self.rows, self.cols, self.format = data, scales, rows, cols, format
-        self.device = data.device
+        self._data, self._scales, self.rows, self.cols, self.format, self.device = data, scales, rows, cols, format, device
         self._c = _MX(data.data_ptr(), scales.data_ptr(), rows, cols, format)
 
     def as_c(self) -> _MX:
@@ -534,7 +537,7 @@ class MXTensor:
     @staticmethod
     def empty(rows: int, cols: int, format: int, device="cuda") -> "MXTensor":
         nd, ns = _mx_bytes(rows, cols, format)  # nd is a multiple of 64
-        buf = torch.empty(nd + ns, dtype=torch.uint8, device=device)
+        buf = torch.empty(nd + ns, dtype=_U8, device=device)
         q = MXTensor.__new__(MXTensor)
         q._data, q._scales, q.rows, q.cols, q.format, q.device = buf, None, rows, cols, format, buf.device
         p = buf.data_ptr()
@@ -542,36 +545,23 @@ class MXTensor:
         return q
 
 
-def _on_stream(fn):
-    """With stream=s, run the call with s (and its device) current, so that what it
-    allocates belongs to s too and may be reused only in s's order."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
-
-
-def _mx_call(name: str, device: torch.device, *args):
-    """Call an MX entry point with `device` current, on its current stream; every
+def _mx_run(fn, name: str, device: torch.device, *args):
+    """Call the entry point `fn` with `device` current, on its current stream; every
     tensor of the call is on that device."""
+    index = device.index
     if device.type != "cuda":
         raise ValueError(f"{name}: tensors have to be on a CUDA device, not {device}")
-    fn = getattr(_lib or load_library(), name)
-    index = device.index
     if index == torch.cuda.current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
             status = fn(*args, _raw_stream(index))
-    if status != QLORA_OK:
+    if status:
         raise QloraError(status, name)
 
 
 def _mx_bf16(t: torch.Tensor, shape: tuple, device, what: str):
-    if t.dtype != torch.bfloat16 or t.shape != shape or not t.is_contiguous() or t.device != device:
+    if t.dtype != _BF16 or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{what} has to be a contiguous bfloat16 tensor of shape {tuple(shape)} on {device}")
 
 
@@ -589,35 +579,42 @@ def qlora_mx_storage_bytes(format: int, rows: int, cols: int) -> tuple:
     return int(out[0]), int(out[1])
 
 
-@_on_stream
-def qlora_quantize_mx(X: torch.Tensor, format: int, out: MXTensor | None = None) -> MXTensor:
+def qlora_quantize_mx(X: torch.Tensor, format: int, out: MXTensor | None = None, stream=None) -> MXTensor:
     """bf16 [rows, cols] (a weight or activations) to MX blocks of 32 along the columns."""
+    if stream is not None:  # what the call allocates then belongs to that stream
+        with torch.cuda.stream(stream):
+            return qlora_quantize_mx(X, format, out)
     shape, dev = X.shape, X.device
     if len(shape) != 2:
         raise ValueError("qlora_quantize_mx takes a matrix")
     _mx_bf16(X, shape, dev, "X")
     out = _mx_out(out, shape, format, dev)
-    _mx_call("qlora_quantize_mx", dev, X.data_ptr(), out._c)
+    _mx_run((_lib or load_library()).qlora_quantize_mx, "qlora_quantize_mx", dev, X.data_ptr(), out._c)
     return out
 
 
-@_on_stream
-def qlora_dequantize_mx(q: MXTensor, out: torch.Tensor | None = None) -> torch.Tensor:
+def qlora_dequantize_mx(q: MXTensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The bf16 values of an MX matrix."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qlora_dequantize_mx(q, out)
+    dev = q.device
     if out is None:
-        out = torch.empty(q.rows, q.cols, dtype=torch.bfloat16, device=q.device)
+        out = torch.empty(q.rows, q.cols, dtype=_BF16, device=dev)
     else:
-        _mx_bf16(out, (q.rows, q.cols), q.device, "out")
-    _mx_call("qlora_dequantize_mx", q.device, q._c, out.data_ptr())
+        _mx_bf16(out, (q.rows, q.cols), dev, "out")
+    _mx_run((_lib or load_library()).qlora_dequantize_mx, "qlora_dequantize_mx", dev, q._c, out.data_ptr())
     return out
 
 
-@_on_stream
 def qlora_rmsnorm_mx(X: torch.Tensor, gamma: torch.Tensor, eps: float, format: int = MX_E4M3,
                      residual: torch.Tensor | None = None, out: MXTensor | None = None,
-                     residual_out: torch.Tensor | None = None):
+                     residual_out: torch.Tensor | None = None, stream=None):
     """RMS norm of X + residual as MX blocks. Returns (MXTensor, the sum in bf16 or
     None without a residual); pass residual_out=residual to update it in place."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qlora_rmsnorm_mx(X, gamma, eps, format, residual, out, residual_out)
     shape, dev = X.shape, X.device
     if len(shape) != 2:
         raise ValueError("qlora_rmsnorm_mx takes a matrix")
@@ -628,12 +625,13 @@ def qlora_rmsnorm_mx(X: torch.Tensor, gamma: torch.Tensor, eps: float, format: i
     else:
         _mx_bf16(residual, shape, dev, "residual")
         if residual_out is None:
-            residual_out = torch.empty_like(residual)
+            residual_out = torch.empty(shape, dtype=_BF16, device=dev)
         else:
             _mx_bf16(residual_out, shape, dev, "residual_out")
         rp, op = residual.data_ptr(), residual_out.data_ptr()
     out = _mx_out(out, shape, format, dev)
-    _mx_call("qlora_rmsnorm_mx", dev, X.data_ptr(), rp, gamma.data_ptr(), eps, out._c, op)
+    _mx_run((_lib or load_library()).qlora_rmsnorm_mx, "qlora_rmsnorm_mx", dev, X.data_ptr(), rp, gamma.data_ptr(),
+            eps, out._c, op)
     return out, residual_out
 
 
@@ -641,66 +639,74 @@ _mx_need = {}      # workspace bytes by call and sizes, as the library's size qu
 _mx_untouched = {}  # device: 256 bytes that stand for the workspace of calls that use none of it
 
 
-def _mx_workspace(name: str, device, x_format: int, rows: int, w: MXTensor, grouped: tuple) -> torch.Tensor:
-    key = (name, x_format, rows, w.rows, w.cols, grouped[1:])
+def _mx_workspace(fn, key: tuple, device, *args) -> tuple:
+    """(tensor, size) for a quantizing product; args: its arguments between X and Y."""
     need = _mx_need.get(key)
     if need is None:
         size = ctypes.c_size_t(0)
-        _mx_call(name, device, None, rows, x_format, w._c, *grouped, None, None, ctypes.byref(size))
+        _mx_run(fn, "workspace query", device, None, *args, None, None, ctypes.byref(size))
         if len(_mx_need) >= 4096:
             _mx_need.clear()
-        need = _mx_need[key] = size.value
-    if need > 256:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        need = _mx_need[key] = (size.value, ctypes.pointer(ctypes.c_size_t(size.value)))
+    if need[0] > 256:
+        return torch.empty(need[0], dtype=_U8, device=device), need[1]
     ws = _mx_untouched.get(device)
     if ws is None:
-        ws = _mx_untouched[device] = torch.empty(256, dtype=torch.uint8, device=device)
-    return ws
+        ws = _mx_untouched[device] = torch.empty(256, dtype=_U8, device=device)
+    return ws, need[1]
+
+
+def qlora_mx_linear_fwd(x: MXTensor | torch.Tensor, w: MXTensor, Y: torch.Tensor | None = None,
+                        x_format: int = MX_E4M3, stream=None) -> torch.Tensor:
+    """Y = x w^T (bf16) with w an MX_E2M1 weight [N, K]. x: an MXTensor [M, K], or bf16
+    activations, which the call quantizes to x_format first."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qlora_mx_linear_fwd(x, w, Y, x_format)
+    return _mx_product("qlora_mx_linear_fwd", x, w, w.rows, Y, x_format)
+
+
+def qlora_mx_grouped_fwd(x: MXTensor | torch.Tensor, w: MXTensor, offsets: torch.Tensor,
+                         Y: torch.Tensor | None = None, x_format: int = MX_E4M3, stream=None) -> torch.Tensor:
+    """Rows offsets[e] .. offsets[e + 1] of x times expert e's weight, rows e N .. (e + 1) N
+    of w (offsets: device int32 [experts + 1]). Rows of Y outside the offsets are not
+    written. x as in qlora_mx_linear_fwd."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return qlora_mx_grouped_fwd(x, w, offsets, Y, x_format)
+    groups = offsets.numel() - 1
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or groups < 1 or not offsets.is_contiguous() or \
+            offsets.device != w.device:
+        raise ValueError(f"offsets have to be contiguous int32 [experts + 1] on {w.device}")
+    if w.rows == 0 or w.rows % groups:
+        raise ValueError(f"a weight of {w.rows} rows is not {groups} experts of equal size")
+    return _mx_product("qlora_mx_grouped_fwd", x, w, w.rows // groups, Y, x_format, offsets.data_ptr(), groups)
 
 
 def _mx_product(name: str, x, w: MXTensor, n: int, Y, x_format: int, *grouped) -> torch.Tensor:
     """The two products' common part: x an MXTensor, or bf16 activations for the quantizing entry point."""
-    dev = w.device
+    lib, dev = _lib or load_library(), w.device
     mx = isinstance(x, MXTensor)
-    rows, cols = (x.rows, x.cols) if mx else x.shape if x.dim() == 2 else (-1, -1)
+    if mx:
+        rows, cols = x.rows, x.cols
+    else:
+        _require(x.dim() == 2 and x.dtype == _BF16 and x.is_contiguous(),
+                 f"{name}: activations are an MXTensor or a contiguous bfloat16 matrix")
+        rows, cols = x.shape
     if cols != w.cols or x.device != dev:
         raise ValueError(f"{name}: activations [{rows}, {cols}] on {x.device} do not match a weight "
                          f"[{w.rows}, {w.cols}] on {dev}")
     if Y is None:
-        Y = torch.empty(rows, n, dtype=torch.bfloat16, device=dev)
+        Y = torch.empty(rows, n, dtype=_BF16, device=dev)
     else:
         _mx_bf16(Y, (rows, n), dev, "Y")
     if mx:
-        _mx_call(name, dev, x._c, w._c, *grouped, Y.data_ptr())
+        _mx_run(getattr(lib, name), name, dev, x._c, w._c, *grouped, Y.data_ptr())
         return Y
-    _mx_bf16(x, (rows, cols), dev, "x")
-    ws = _mx_workspace(name + "_bf16", dev, x_format, rows, w, grouped)
-    _mx_call(name + "_bf16", dev, x.data_ptr(), rows, x_format, w._c, *grouped, Y.data_ptr(), ws.data_ptr(),
-             ctypes.byref(ctypes.c_size_t(ws.numel())))
+    fn = lib.qlora_mx_grouped_fwd_bf16 if grouped else lib.qlora_mx_linear_fwd_bf16
+    ws, size = _mx_workspace(fn, (rows, n, cols, w.rows, x_format, len(grouped)), dev, rows, x_format, w._c, *grouped)
+    _mx_run(fn, name, dev, x.data_ptr(), rows, x_format, w._c, *grouped, Y.data_ptr(), ws.data_ptr(), size)
     return Y
-
-
-@_on_stream
-def qlora_mx_linear_fwd(x: MXTensor | torch.Tensor, w: MXTensor, Y: torch.Tensor | None = None,
-                        x_format: int = MX_E4M3) -> torch.Tensor:
-    """Y = x w^T (bf16) with w an MX_E2M1 weight [N, K]. x: an MXTensor [M, K], or bf16
-    activations, which the call quantizes to x_format first."""
-    return _mx_product("qlora_mx_linear_fwd", x, w, w.rows, Y, x_format)
-
-
-@_on_stream
-def qlora_mx_grouped_fwd(x: MXTensor | torch.Tensor, w: MXTensor, offsets: torch.Tensor,
-                         Y: torch.Tensor | None = None, x_format: int = MX_E4M3) -> torch.Tensor:
-    """Rows offsets[e] .. offsets[e + 1] of x times expert e's weight, rows e N .. (e + 1) N
-    of w (offsets: device int32 [experts + 1]). Rows of Y outside the offsets are not
-    written. x as in qlora_mx_linear_fwd."""
-    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous() \
-            or offsets.device != w.device:
-        raise ValueError(f"offsets have to be contiguous int32 [experts + 1] on {w.device}")
-    groups = offsets.numel() - 1
-    if w.rows == 0 or w.rows % groups:
-        raise ValueError(f"a weight of {w.rows} rows is not {groups} experts of equal size")
-    return _mx_product("qlora_mx_grouped_fwd", x, w, w.rows // groups, Y, x_format, offsets.data_ptr(), groups)
 
 
 def qlora_device_error(stream=None) -> int:
