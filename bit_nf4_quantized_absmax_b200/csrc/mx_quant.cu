@@ -151,41 +151,72 @@ k_mx_dequantize(const uint8_t* __restrict__ data, const uint8_t* __restrict__ sc
   }
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 1 / sqrt(v) as a head and a tail, to about 2^-43: the fp32 estimate and one Newton
+// step in fp64 (an fp64 division and root in every thread took a third of the
+// norm's time).
+__device__ __forceinline__ void rsqrt_head_tail(double v, float& hi, float& lo) {
+  double r;
+  if (v > 1e-35 && v < 1e38) {
+    const double e = static_cast<double>(rsqrtf(static_cast<float>(v)));
+    r = e * (1.5 - 0.5 * v * e * e);
+  } else {
+    r = 1.0 / sqrt(v);
+  }
+  hi = static_cast<float>(r);
+  lo = static_cast<float>(r - static_cast<double>(hi));
+  if (!(fabsf(hi) < __int_as_float(0x7F800000))) lo = 0.0f;  // infinite or NaN
+}
+
 // h = bf16(x + residual) (or x), rstd = 1 / sqrt(mean(h^2) + eps), y = h rstd
-// gamma, y to MX blocks: one CTA a row, the row read once and kept in registers
+// gamma, y to MX blocks: a CTA a row, the row read once and kept in registers
 // (8 elements a chunk, CHUNKS chunks a thread), so x and the residual cross
-// memory once in and the sum and the codes once out.
+// memory once in and the sum and the codes once out. A CTA takes every gridDim-th
+// row, reads the next one before it reduces the present one, and keeps gamma.
 //
-// The squares of bf16 values are exact in fp32; a thread adds at most 32 of them
-// in fp32 and the rest of the sum, the mean and rstd are fp64 (a few operations
-// a row). h * gamma is exact in fp32 too, and rstd enters as a head and a tail,
+// The squares of bf16 values are exact in fp32; a thread adds at most 16 + 16 of
+// them in fp32 and the rest of the sum, the mean and rstd are fp64 (a few operations
+// a warp). h * gamma is exact in fp32 too, and rstd enters as a head and a tail,
 // so y carries one fp32 rounding before it is quantized. Four neighbouring
 // lanes hold a block; the sixteen lanes of 128 elements make a scale word.
 template <int FMT, int CHUNKS, bool RES>
 __global__ void __launch_bounds__(1024)
 k_rmsnorm_mx(const uint4* __restrict__ X, const uint4* residual, const uint4* __restrict__ gamma, float eps,
              int64_t rows, int cols, uint4* residual_out, uint8_t* __restrict__ data, uint32_t* __restrict__ scales) {
-  __shared__ double warp_sum[32];
+  __shared__ double warp_sum[2][32];
   const int T = blockDim.x;
   const int kp = (cols + 127) / 128 * 128;
   const int nchunk = cols / 8, nchunk_p = kp / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const double inv_cols = 1.0 / cols;
   pdl_enter();
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    const int64_t base = row * nchunk;
-    // every load of the row before the first store: residual_out may be residual
-    uint4 xq[CHUNKS], rq[CHUNKS];
+  uint4 xq[CHUNKS], rq[CHUNKS], gq[CHUNKS];
+  auto load = [&](int64_t row) {
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
       const int i = c * T + threadIdx.x;
       xq[c] = rq[c] = make_uint4(0u, 0u, 0u, 0u);
-      if (i < nchunk) {
-        xq[c] = __ldcs(X + base + i);
-        if (RES) rq[c] = __ldcs(residual + base + i);
+      if (i < nchunk && row < rows) {
+        xq[c] = __ldcs(X + row * nchunk + i);
+        if (RES) rq[c] = __ldcs(residual + row * nchunk + i);
       }
     }
+  };
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int i = c * T + threadIdx.x;
+    gq[c] = i < nchunk ? __ldg(gamma + i) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  load(blockIdx.x);
+  int buf = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, buf ^= 1) {
     uint32_t h[CHUNKS][4];
-    float ss = 0.0f;
+    f32x2 sq = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
       const int i = c * T + threadIdx.x;
@@ -199,43 +230,40 @@ k_rmsnorm_mx(const uint4* __restrict__ X, const uint4* residual, const uint4* __
         for (int j = 0; j < 4; ++j)
           h[c][j] = pack_bf16x2(bf16lo_to_f32(h[c][j]) + bf16lo_to_f32(rr[j]),
                                 bf16hi_to_f32(h[c][j]) + bf16hi_to_f32(rr[j]));
-        if (i < nchunk) residual_out[base + i] = make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
+        if (i < nchunk) residual_out[row * nchunk + i] = make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = bf16lo_to_f32(h[c][j]), b = bf16hi_to_f32(h[c][j]);
-        ss = __fmaf_rn(a, a, ss);
-        ss = __fmaf_rn(b, b, ss);
+        const f32x2 a = {bf16lo_to_f32(h[c][j]), bf16hi_to_f32(h[c][j])};
+        sq = fma_f32x2(a, a, sq);
       }
     }
-    double d = ss;
+    load(row + gridDim.x);
+    double d = static_cast<double>(sq.x) + static_cast<double>(sq.y);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    if (lane == 0) warp_sum[warp] = d;
-    __syncthreads();
-    d = 0.0;
-    for (int w = 0; w < T / 32; ++w) d += warp_sum[w];  // the same order in every thread
-    __syncthreads();                                    // before the next row writes it
-    const double rstd = 1.0 / sqrt(d / cols + static_cast<double>(eps));
-    const float r_hi = static_cast<float>(rstd);
-    const float r_lo = static_cast<float>(rstd - static_cast<double>(r_hi));
+    if (lane == 0) warp_sum[buf][warp] = d;
+    __syncthreads();  // one a row: the row after next is the first to write this half again
+    d = lane < T / 32 ? warp_sum[buf][lane] : 0.0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);  // the same order in every warp
+    float r_hi, r_lo;
+    rsqrt_head_tail(d * inv_cols + static_cast<double>(eps), r_hi, r_lo);
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
       const int i = c * T + threadIdx.x;
       const bool valid = i < nchunk;
-      uint4 g = make_uint4(0u, 0u, 0u, 0u);
-      if (valid) g = __ldg(gamma + i);
-      const uint32_t gg[4] = {g.x, g.y, g.z, g.w};
-      float y[8];
-      uint32_t m = 0u;
+      const uint32_t gg[4] = {gq[c].x, gq[c].y, gq[c].z, gq[c].w};
+      f32x2 y[4];
+      float big = 0.0f;  // of the magnitudes; NaN where one is
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = bf16lo_to_f32(h[c][j]) * bf16lo_to_f32(gg[j]);
-        const float b = bf16hi_to_f32(h[c][j]) * bf16hi_to_f32(gg[j]);
-        y[2 * j] = valid ? __fmaf_rn(a, r_hi, a * r_lo) : 0.0f;
-        y[2 * j + 1] = valid ? __fmaf_rn(b, r_hi, b * r_lo) : 0.0f;
-        m = max(m, max(__float_as_uint(y[2 * j]) & 0x7FFFFFFFu, __float_as_uint(y[2 * j + 1]) & 0x7FFFFFFFu));
+        const f32x2 a = mul_f32x2({bf16lo_to_f32(h[c][j]), bf16hi_to_f32(h[c][j])},
+                                  {bf16lo_to_f32(gg[j]), bf16hi_to_f32(gg[j])});
+        y[j] = fma_f32x2(a, {r_hi, r_hi}, mul_f32x2(a, {r_lo, r_lo}));
+        big = max_nan(big, max_nan(fabsf(y[j].x), fabsf(y[j].y)));
       }
+      uint32_t m = __float_as_uint(big);
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const uint32_t byte = valid ? mx_scale_byte<FMT>(m >> 23) : 127u;
@@ -246,16 +274,21 @@ k_rmsnorm_mx(const uint4* __restrict__ X, const uint4* residual, const uint4* __
       if (i >= nchunk_p) continue;
       if ((lane & 15) == 0) scales[static_cast<int64_t>(i >> 4) * rows + row] = word;
       const float inv = mx_inverse_scale(byte);
-      const bool bad = byte == 255u;
+      const bool zero = byte == 255u || !valid;
+      float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] *= inv;
+      for (int j = 0; j < 4; ++j) {
+        y[j] = mul_f32x2(y[j], {inv, inv});
+        v[2 * j] = y[j].x;
+        v[2 * j + 1] = y[j].y;
+      }
       if (FMT == kMxE4M3) {
-        uint2 o = make_uint2(cvt_e4m3x2(y[0], y[1]) | (cvt_e4m3x2(y[2], y[3]) << 16),
-                             cvt_e4m3x2(y[4], y[5]) | (cvt_e4m3x2(y[6], y[7]) << 16));
-        if (bad) o = make_uint2(0u, 0u);
+        uint2 o = make_uint2(cvt_e4m3x2(v[0], v[1]) | (cvt_e4m3x2(v[2], v[3]) << 16),
+                             cvt_e4m3x2(v[4], v[5]) | (cvt_e4m3x2(v[6], v[7]) << 16));
+        if (zero) o = make_uint2(0u, 0u);
         *reinterpret_cast<uint2*>(data + row * kp + static_cast<int64_t>(i) * 8) = o;
       } else {
-        *reinterpret_cast<uint32_t*>(data + (row * kp + static_cast<int64_t>(i) * 8) / 2) = bad ? 0u : cvt_e2m1x8(y);
+        *reinterpret_cast<uint32_t*>(data + (row * kp + static_cast<int64_t>(i) * 8) / 2) = zero ? 0u : cvt_e2m1x8(v);
       }
     }
   }
@@ -271,11 +304,13 @@ template <int FMT, bool RES>
 cudaError_t run_rmsnorm(const void* X, const void* residual, const void* gamma, float eps, const MxView& q,
                         void* residual_out, int num_sms, cudaStream_t stream) {
   const int nchunk_p = static_cast<int>((q.cols + 127) / 128 * 16);
-  int chunks = 1;
-  while (nchunk_p > 1024 * chunks) chunks *= 2;
+  // Two chunks a thread halve what a row's sum costs against its elements (4096x4096 with a residual: 23.9 us with one,
+  // 22.5 with two, 33.1 with four, whose registers leave half of the threads); four only where two would need more than
+  // 512 threads.
+  const int chunks = nchunk_p <= 64 ? 1 : (nchunk_p <= 1024 ? 2 : 4);
   const int threads = ((nchunk_p + chunks - 1) / chunks + 31) / 32 * 32;
-  const int64_t cap = static_cast<int64_t>(num_sms) * 64;
-  const int grid = static_cast<int>(q.rows < cap ? q.rows : cap);
+  const int64_t resident = static_cast<int64_t>(num_sms) * (2048 / threads < 16 ? 2048 / threads : 16);
+  const int grid = static_cast<int>(q.rows < resident ? q.rows : resident);
   auto kern = chunks == 1 ? k_rmsnorm_mx<FMT, 1, RES> : (chunks == 2 ? k_rmsnorm_mx<FMT, 2, RES> : k_rmsnorm_mx<FMT, 4, RES>);
   return launch_pdl(kern, dim3(grid), dim3(threads), 0, stream, reinterpret_cast<const uint4*>(X),
                     reinterpret_cast<const uint4*>(residual), reinterpret_cast<const uint4*>(gamma), eps, q.rows,
