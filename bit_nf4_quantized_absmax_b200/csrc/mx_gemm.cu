@@ -642,23 +642,23 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 // product. A tile at the end of a group is only as wide as its rows need
 // (a multiple of 32): its MMAs and loads shrink with it.
 //
-// The accumulator takes 256 TMEM columns and the scales 72 more, so there is one
+// The accumulator takes 256 TMEM columns and the scales 192 more, so there is one
 // accumulator; the epilogue's eight warps move it to registers (rounded to bf16, 64
 // registers a thread) and release it before they store, which keeps the pause of
 // the MMAs to the TMEM reads.
 //
-// The scales have a ring of their own, of blocks of four k-blocks: two warps of each
-// CTA store them (fence, arrive) once per block and three blocks ahead. Per k-block
-// and in step with the data these took 1250 clocks a k-block, most of it the release
-// at cluster scope with which the odd CTA's words reach the leader's barrier; now
-// that release (by a relay warp, which has no loads in flight to wait for) is one in
-// four k-blocks and has some 6000 clocks to arrive.
+// The scales have a ring of their own, of blocks of eight k-blocks: two warps of each
+// CTA store them (fence, arrive) once per block and a block ahead. The odd CTA's words
+// reach the leader's barrier by a release at cluster scope, from a warp that has no
+// loads in flight to wait for: it takes 1000 to 1600 clocks, which bounded the product
+// while there was one in one k-block (1250 clocks a k-block) or in four (410).
 constexpr int kPairMaxStages = 10;
 constexpr int kPairRing = 6 * (kMxRows + 128) * kMxBK;  // bytes of the operands' ring: 6 stages of the widest tile
 constexpr int kPairThreads = 384;  // warps: TMA, MMA (odd CTA: relay), scales of w, scales of x, eight for the epilogue
 constexpr int kPairW = kMxRows * kMxBK;
-constexpr int kPairSfDepth = 4;    // k-blocks a block of scales
-constexpr int kPairSfSlots = 3;
+constexpr int kPairBatch = 4;      // k-blocks that one elected region issues
+constexpr int kPairSfDepth = 8;    // k-blocks a block of scales
+constexpr int kPairSfSlots = 2;
 constexpr int kPairSfOne = 512 + 1024;  // bytes a k-block: words of 128 weight rows, of 256 tokens
 constexpr int kPairSfSlot = kPairSfDepth * kPairSfOne;
 constexpr int kPairOut = 1024;          // bytes an epilogue warp stages: 16 tokens of 32 weight rows
@@ -820,6 +820,7 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   if (warp == 0) {
     // ---------------- TMA (both CTAs; the bytes count on the leader's barrier) ----------------
     const uint32_t fbar0 = map_to_cta(smem_u32(full), 0);
+    const bool leader = elect_one();
     int stage = 0;
     uint32_t phase = 0;
     int64_t issued = 0;
@@ -831,15 +832,15 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       const int32_t wrow = static_cast<int32_t>(t.w0 + rank * 128);
       const int32_t xrow = static_cast<int32_t>(t.row0 + rank * half);
       const uint32_t bytes = 2 * (kPairW / 2 + half * (a.x_fp4 ? kMxBK / 2 : kMxBK));
-      if (elect_one()) {
-        int st = stage;
-        uint32_t ph = phase;
-        for (int kb = 0; kb < a.nkb && ok; ++kb) {
-          ok = wait_or_abort(&empty[st], ph ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY);
-          if (!ok) break;
-          uint8_t* sw = smem + st * a.stage_bytes;
-          if (rank == 0) mbar_arrive_expect_tx(&full[st], bytes);
-          const uint32_t fbar = fbar0 + st * 8;
+      // The warp stays converged and only the copies are the elected lane's: within `if (elect_one())` around the loop the
+      // copies' operands left the uniform registers (tiles of 64 tokens: 8% slower).
+      for (int kb = 0; kb < a.nkb && ok; ++kb) {
+        ok = wait_or_abort(&empty[stage], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY);
+        if (!ok) break;
+        uint8_t* sw = smem + stage * a.stage_bytes;
+        const uint32_t fbar = fbar0 + stage * 8;
+        if (leader) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
           tma_load_2d_pair(sw, &tm_w, fbar, kb * kMxBK, wrow);
           int at = 0;
 #pragma unroll
@@ -849,21 +850,19 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
               at += 128 >> b;
             }
           }
-          if (++st == a.stages) {
-            st = 0;
-            ph ^= 1u;
-          }
+        }
+        __syncwarp();  // no lane may fall two phases behind the barrier that it waits on
+        ++issued;
+        if (++stage == a.stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
       __syncwarp();
       ok = __all_sync(0xffffffffu, ok);
-      issued += a.nkb;  // (after an abort the waits below just run out)
-      const int turns = (stage + a.nkb) / a.stages;
-      stage = stage + a.nkb - turns * a.stages;
-      phase ^= turns & 1;
     }
     // after an abort, let the copies already issued land before the pair leaves
-    if (lane == 0 && rank == 0 && *abort_flag)
+    if (leader && rank == 0 && *abort_flag)
       for (int64_t i = max(static_cast<int64_t>(0), issued - a.stages); i < issued; ++i)
         mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, err, DEV_TIMEOUT_TMA_FULL);
   } else if (warp == 1) {
@@ -889,46 +888,49 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
           ok = __all_sync(0xffffffffu,
                           wait_or_abort_cluster(&sf_full[slot], sf_phase, abort_flag, err, DEV_TIMEOUT_TMA_FULL));
           if (!ok) break;
-          int st[kPairSfDepth];
-          uint32_t ph[kPairSfDepth];
+          const int end = min(a.nkb, base + kPairSfDepth);
+          for (int kb0 = base; kb0 < end && ok; kb0 += kPairBatch) {
+            int st[kPairBatch];
+            uint32_t ph[kPairBatch];
 #pragma unroll
-          for (int i = 0; i < kPairSfDepth; ++i) {
-            st[i] = stage;
-            ph[i] = phase;
-            if (base + i < a.nkb && ++stage == a.stages) {
-              stage = 0;
-              phase ^= 1u;
-            }
-          }
-          if (elect_one()) {
-            bool good = true;
-#pragma unroll
-            for (int i = 0; i < kPairSfDepth; ++i) {
-              if (base + i < a.nkb && good) {
-                good = wait_or_abort(&full[st[i]], ph[i], abort_flag, err, DEV_TIMEOUT_TMA_FULL);
-                if (good) {
-                  tc_fence_after();
-                  const uint64_t at = static_cast<uint32_t>(st[i] * a.stage_bytes) >> 4;
-                  const uint32_t one = slot * kPairSfDepth + i;  // this k-block's place among the scales
-                  const uint64_t df = df0 + one * (kPairSfOne >> 4);
-                  // TMEM columns of its own: the MMAs that read them last have completed, or the slot would not have
-                  // been refilled
-                  const uint32_t tsf = tmem_base + kPairSfCol + kPairSfCols * one;
-                  tmem_copy_scales_pair(tsf, df);
-                  tmem_copy_scales_pair(tsf + 4, df + (512 >> 4));
-                  if (wide) tmem_copy_scales_pair(tsf + 8, df + (1024 >> 4));
-#pragma unroll
-                  for (uint32_t j = 0; j < kMxBK / 32; ++j)
-                    mma_mx_pair(tmem_base, dw0 + at + j * 2, dx0 + at + j * 2, idesc | (j << 4) | (j << 29), tsf,
-                                tsf + 4, (base + i > 0 || j > 0) ? 1u : 0u);
-                  mma_commit_pair(&empty[st[i]]);
-                }
+            for (int i = 0; i < kPairBatch; ++i) {
+              st[i] = stage;
+              ph[i] = phase;
+              if (kb0 + i < end && ++stage == a.stages) {
+                stage = 0;
+                phase ^= 1u;
               }
             }
-            if (good) mma_commit_pair(&sf_empty[slot]);
+            if (elect_one()) {
+              bool good = true;
+#pragma unroll
+              for (int i = 0; i < kPairBatch; ++i) {
+                if (kb0 + i < end && good) {
+                  good = wait_or_abort(&full[st[i]], ph[i], abort_flag, err, DEV_TIMEOUT_TMA_FULL);
+                  if (good) {
+                    tc_fence_after();
+                    const uint64_t at = static_cast<uint32_t>(st[i] * a.stage_bytes) >> 4;
+                    const uint32_t one = slot * kPairSfDepth + (kb0 - base) + i;  // this k-block's place among the scales
+                    const uint64_t df = df0 + one * (kPairSfOne >> 4);
+                    // TMEM columns of its own: the MMAs that read them last have completed, or the slot would not have
+                    // been refilled
+                    const uint32_t tsf = tmem_base + kPairSfCol + kPairSfCols * one;
+                    tmem_copy_scales_pair(tsf, df);
+                    tmem_copy_scales_pair(tsf + 4, df + (512 >> 4));
+                    if (wide) tmem_copy_scales_pair(tsf + 8, df + (1024 >> 4));
+#pragma unroll
+                    for (uint32_t j = 0; j < kMxBK / 32; ++j)
+                      mma_mx_pair(tmem_base, dw0 + at + j * 2, dx0 + at + j * 2, idesc | (j << 4) | (j << 29), tsf,
+                                  tsf + 4, (kb0 + i > 0 || j > 0) ? 1u : 0u);
+                    mma_commit_pair(&empty[st[i]]);
+                  }
+                }
+              }
+              if (good && kb0 + kPairBatch >= end) mma_commit_pair(&sf_empty[slot]);
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, *abort_flag == 0);
           }
-          __syncwarp();
-          ok = __all_sync(0xffffffffu, *abort_flag == 0);
           if (++slot == kPairSfSlots) {
             slot = 0;
             sf_phase ^= 1u;
