@@ -548,9 +548,9 @@ class MXTensor:
 def _mx_run(fn, name: str, device: torch.device, *args):
     """Call the entry point `fn` with `device` current, on its current stream; every
     tensor of the call is on that device."""
-    index = device.index
     if device.type != "cuda":
         raise ValueError(f"{name}: tensors have to be on a CUDA device, not {device}")
+    index = device.index
     if index == torch.cuda.current_device():
         status = fn(*args, _raw_stream(index))
     else:
@@ -565,9 +565,15 @@ def _mx_bf16(t: torch.Tensor, shape: tuple, device, what: str):
         raise ValueError(f"{what} has to be a contiguous bfloat16 tensor of shape {tuple(shape)} on {device}")
 
 
-def _mx_out(out: MXTensor | None, shape: tuple, format: int, device) -> MXTensor:
-    if out is None:
-        return MXTensor.empty(shape[0], shape[1], format, device)
+def _mx_matrix(t: torch.Tensor, what: str) -> tuple:
+    """(shape, device) of a contiguous bf16 matrix."""
+    shape = t.shape
+    if t.dtype != _BF16 or len(shape) != 2 or not t.is_contiguous():
+        raise ValueError(f"{what} has to be a contiguous bfloat16 matrix")
+    return shape, t.device
+
+
+def _mx_out(out: MXTensor, shape: tuple, format: int, device) -> MXTensor:
     if out.rows != shape[0] or out.cols != shape[1] or out.format != format or out.device != device:
         raise ValueError("out has another shape, format or device than the result")
     return out
@@ -584,11 +590,8 @@ def qlora_quantize_mx(X: torch.Tensor, format: int, out: MXTensor | None = None,
     if stream is not None:  # what the call allocates then belongs to that stream
         with torch.cuda.stream(stream):
             return qlora_quantize_mx(X, format, out)
-    shape, dev = X.shape, X.device
-    if len(shape) != 2:
-        raise ValueError("qlora_quantize_mx takes a matrix")
-    _mx_bf16(X, shape, dev, "X")
-    out = _mx_out(out, shape, format, dev)
+    shape, dev = _mx_matrix(X, "X")
+    out = MXTensor.empty(shape[0], shape[1], format, dev) if out is None else _mx_out(out, shape, format, dev)
     _mx_run((_lib or load_library()).qlora_quantize_mx, "qlora_quantize_mx", dev, X.data_ptr(), out._c)
     return out
 
@@ -615,10 +618,7 @@ def qlora_rmsnorm_mx(X: torch.Tensor, gamma: torch.Tensor, eps: float, format: i
     if stream is not None:
         with torch.cuda.stream(stream):
             return qlora_rmsnorm_mx(X, gamma, eps, format, residual, out, residual_out)
-    shape, dev = X.shape, X.device
-    if len(shape) != 2:
-        raise ValueError("qlora_rmsnorm_mx takes a matrix")
-    _mx_bf16(X, shape, dev, "X")
+    shape, dev = _mx_matrix(X, "X")
     _mx_bf16(gamma, shape[1:], dev, "gamma")
     if residual is None:
         residual_out = rp = op = None
@@ -629,7 +629,7 @@ def qlora_rmsnorm_mx(X: torch.Tensor, gamma: torch.Tensor, eps: float, format: i
         else:
             _mx_bf16(residual_out, shape, dev, "residual_out")
         rp, op = residual.data_ptr(), residual_out.data_ptr()
-    out = _mx_out(out, shape, format, dev)
+    out = MXTensor.empty(shape[0], shape[1], format, dev) if out is None else _mx_out(out, shape, format, dev)
     _mx_run((_lib or load_library()).qlora_rmsnorm_mx, "qlora_rmsnorm_mx", dev, X.data_ptr(), rp, gamma.data_ptr(),
             eps, out._c, op)
     return out, residual_out
@@ -690,9 +690,7 @@ def _mx_product(name: str, x, w: MXTensor, n: int, Y, x_format: int, *grouped) -
     if mx:
         rows, cols = x.rows, x.cols
     else:
-        _require(x.dim() == 2 and x.dtype == _BF16 and x.is_contiguous(),
-                 f"{name}: activations are an MXTensor or a contiguous bfloat16 matrix")
-        rows, cols = x.shape
+        rows, cols = _mx_matrix(x, "x, where it is no MXTensor,")[0]
     if cols != w.cols or x.device != dev:
         raise ValueError(f"{name}: activations [{rows}, {cols}] on {x.device} do not match a weight "
                          f"[{w.rows}, {w.cols}] on {dev}")
