@@ -545,6 +545,14 @@ class MXTensor:
         return q
 
 
+def _mx_on(stream, device: torch.device):
+    """Make `stream` (of the tensors' device) the current one: what the call allocates then belongs to it too, and may be
+    reused only in its order."""
+    if stream.device != device:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
+    return torch.cuda.stream(stream)
+
+
 def _mx_run(fn, name: str, device: torch.device, *args):
     """Call the entry point `fn` with `device` current, on its current stream; every
     tensor of the call is on that device."""
@@ -587,8 +595,8 @@ def qlora_mx_storage_bytes(format: int, rows: int, cols: int) -> tuple:
 
 def qlora_quantize_mx(X: torch.Tensor, format: int, out: MXTensor | None = None, stream=None) -> MXTensor:
     """bf16 [rows, cols] (a weight or activations) to MX blocks of 32 along the columns."""
-    if stream is not None:  # what the call allocates then belongs to that stream
-        with torch.cuda.stream(stream):
+    if stream is not None:
+        with _mx_on(stream, X.device):
             return qlora_quantize_mx(X, format, out)
     shape, dev = _mx_matrix(X, "X")
     out = MXTensor.empty(shape[0], shape[1], format, dev) if out is None else _mx_out(out, shape, format, dev)
@@ -599,7 +607,7 @@ def qlora_quantize_mx(X: torch.Tensor, format: int, out: MXTensor | None = None,
 def qlora_dequantize_mx(q: MXTensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The bf16 values of an MX matrix."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _mx_on(stream, q.device):
             return qlora_dequantize_mx(q, out)
     dev = q.device
     if out is None:
@@ -616,7 +624,7 @@ def qlora_rmsnorm_mx(X: torch.Tensor, gamma: torch.Tensor, eps: float, format: i
     """RMS norm of X + residual as MX blocks. Returns (MXTensor, the sum in bf16 or
     None without a residual); pass residual_out=residual to update it in place."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _mx_on(stream, X.device):
             return qlora_rmsnorm_mx(X, gamma, eps, format, residual, out, residual_out)
     shape, dev = _mx_matrix(X, "X")
     _mx_bf16(gamma, shape[1:], dev, "gamma")
@@ -661,7 +669,7 @@ def qlora_mx_linear_fwd(x: MXTensor | torch.Tensor, w: MXTensor, Y: torch.Tensor
     """Y = x w^T (bf16) with w an MX_E2M1 weight [N, K]. x: an MXTensor [M, K], or bf16
     activations, which the call quantizes to x_format first."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _mx_on(stream, w.device):
             return qlora_mx_linear_fwd(x, w, Y, x_format)
     return _mx_product("qlora_mx_linear_fwd", x, w, w.rows, Y, x_format)
 
@@ -672,7 +680,7 @@ def qlora_mx_grouped_fwd(x: MXTensor | torch.Tensor, w: MXTensor, offsets: torch
     of w (offsets: device int32 [experts + 1]). Rows of Y outside the offsets are not
     written. x as in qlora_mx_linear_fwd."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _mx_on(stream, w.device):
             return qlora_mx_grouped_fwd(x, w, offsets, Y, x_format)
     groups = offsets.numel() - 1
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or groups < 1 or not offsets.is_contiguous() or \

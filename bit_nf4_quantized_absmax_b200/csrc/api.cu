@@ -163,7 +163,7 @@ qlora_status check_mx_product(const qlora_mx_tensor* w, int64_t M, int64_t K, in
   }
   const qlora_status st = check_mx(w);
   if (st != QLORA_OK) return st;
-  if (w->format != QLORA_MX_E2M1) return QLORA_ERR_UNSUPPORTED;
+  if (w->format != QLORA_MX_E2M1 || w->cols > kMxMaxK) return QLORA_ERR_UNSUPPORTED;
   if (K != w->cols || w->rows == 0 || w->rows % groups) return QLORA_ERR_INVALID_ARG;
   return mx_gemm_fits(M, w->rows / groups, groups) ? QLORA_OK : QLORA_ERR_UNSUPPORTED;
 }

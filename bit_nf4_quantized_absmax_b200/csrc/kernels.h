@@ -207,6 +207,7 @@ cudaError_t launch_rmsnorm_mx(const void* X, const void* residual, const void* g
 // of rows [e N, (e+1) N) of w, for e < groups; offsets null: one group of all rows.
 // x_bf16, where mx_gemm_quantizes() says so, stands for x's storage.
 constexpr int kMxMaxGroups = 4096;
+constexpr int64_t kMxMaxK = int64_t(1) << 20;  // a tile's time stays far below the bound of the kernels' waits
 // Whether the product's grid and tile indices stay within their ranges.
 bool mx_gemm_fits(int64_t M, int64_t N, int64_t groups);
 bool mx_gemm_quantizes(int64_t M, int64_t groups);

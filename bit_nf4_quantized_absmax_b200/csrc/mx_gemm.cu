@@ -9,10 +9,20 @@
 //
 // Operand stages hold 128 elements of k. e4m3 rows are copied as they are; e2m1
 // rows are widened by TMA to the 8-bit containers that this MMA kind reads (16
-// codes become 8 bytes of codes and 8 of padding), so both take 128 bytes a row
-// and one swizzle. Scale words (4 bytes: the row's 4 blocks of the stage) are
-// read four stages ahead into registers and stored where tcgen05.cp wants them: row r of 128 at byte (r % 32) * 16 + (r / 32) * 4. The
-// MMA of block j reads byte j of each word.
+// codes become 8 bytes of codes and 8 of padding; a copy counts the codes' bytes),
+// so both take 128 bytes a row and one swizzle. Scale words (4 bytes: the row's 4
+// blocks of the stage) are read ahead into registers and stored where tcgen05.cp
+// wants them: row r of 128 at byte (r % 32) * 16 + (r / 32) * 4. The MMA of block j
+// reads byte j of each word.
+//
+// Two kernels: k_mx_gemm, one tile a CTA or a cluster, for few tokens and for as many
+// tiles as there are SMs; k_mx_gemm_pair, persistent CTA pairs, beyond. Measured on
+// the device (x already MX, weights in rotation over three sets):
+//   one token       4096x4096  5.9 us   11008x4096  7.3 us (24 MB: 3.3 TB/s)
+//   512 tokens      4096x4096 11.8 us   11008x4096 25.9 us
+//   4096 tokens     4096x4096 55 us (2500 TFLOP/s)   11008x4096 138 us (2680)
+// The first line is latency (launch, first copies, a reduction over the cluster), the
+// last the MMAs at the clock that 1000 W allow (1300 to 1400 MHz of 1965).
 #include <cuda.h>
 
 #include "common.cuh"
@@ -26,7 +36,7 @@ namespace {
 
 constexpr int kMxBK = 128;     // elements of k a stage
 constexpr int kMxRows = 128;   // weight rows a tile
-constexpr int kMxThreads = 128;   // and four warps more where the kernel quantizes x
+constexpr int kMxThreads = 128;  // and four warps more where the kernel quantizes x
 
 // Scale words are handled four k-blocks at a time, in a ring of two such blocks: a
 // warp's stores, fence and arrival take some 300 clocks, as long as a k-block's
@@ -100,8 +110,9 @@ __device__ __forceinline__ bool elect_one() {
 
 // The scale words of GROUPS x 128 rows from r0 on, for the k-blocks of a tile, kept
 // AHEAD stages ahead in a warp's registers: lane l holds rows l, l + 32, l + 64 and
-// l + 96 of each 128, the 16 bytes that tcgen05.cp wants together. Rows at or past
-// `rows` (and groups past `groups`) read as 0.
+// l + 96 of each 128, the 16 bytes that tcgen05.cp wants together. Rows past `count` or
+// at or past `rows` read as 0. (cp.async instead of registers: the proxy fence after it
+// waited for all that were in flight, 20% of a large product.)
 template <int GROUPS, int AHEAD>
 struct ScaleWords {
   uint32_t w[AHEAD][GROUPS * 4];
@@ -354,8 +365,9 @@ __device__ __forceinline__ void quantize_stages(const MxArgs& a, int64_t row0, i
 // adds up its share of the tokens over the cluster, in the order of the CTAs.
 //
 // QUANT (TN = 16): x is bf16, and four more warps write the tokens' side of the stages
-// themselves, so that a decode step is one launch and its activations are never stored. A few tokens are quantized again by every CTA,
-// which costs less than a launch and a round trip through memory.
+// themselves, so that a decode step is one launch and its activations are never
+// stored. A few tokens are quantized again by every CTA, which costs less (one token
+// 0.8 us, 16 tokens 2 us) than a launch and a round trip through memory.
 template <int TN, bool QUANT, bool DEEP>
 __global__ void __launch_bounds__(QUANT ? kMxThreads + 128 : kMxThreads)
 k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x, const MxArgs a,
@@ -636,11 +648,12 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 // ---------------------------------------------------------------------------
 // Many tokens: persistent CTA pairs, 256 weight rows by up to 256 tokens a tile
 // (cta_group::2: each CTA stages 128 weight rows and half of the tokens, and keeps
-// 128 rows of the accumulator). A stage of the full tile is 24 KB of loads a CTA
-// for 512 clocks of MMA at the 8-bit rate, where a 1-CTA tile of 128 x 128 would
-// need 24 KB for 128: the traffic between L2 and the SMs is what bounds this
-// product. A tile at the end of a group is only as wide as its rows need
-// (a multiple of 32): its MMAs and loads shrink with it.
+// 128 rows of the accumulator). A k-block of the full tile is 24 KB of loads a CTA
+// for 512 clocks of MMA at the 8-bit rate, where a 1-CTA tile of 128 x 128 needs as
+// much for 256 (4096 tokens, 11008x4096: 234 us with those). The rows of a group are
+// cut into tiles of equal width, a multiple of 32, so no MMA is wider than its rows
+// need (8192 rows over 16 experts: 163 us with a remainder tile a group, 135 so).
+// What bounds it at full width is the MMA pipe: 2048 clocks for four k-blocks.
 //
 // The accumulator takes 256 TMEM columns and the scales 192 more, so there is one
 // accumulator; the epilogue's eight warps move it to registers (rounded to bf16, 64
@@ -835,7 +848,9 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       // The warp stays converged and only the copies are the elected lane's: within `if (elect_one())` around the loop the
       // copies' operands left the uniform registers (tiles of 64 tokens: 8% slower).
       for (int kb = 0; kb < a.nkb && ok; ++kb) {
-        ok = wait_or_abort(&empty[stage], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY);
+        // (the vote also keeps every lane within a phase of the barrier that it waits on)
+        ok = __all_sync(0xffffffffu,
+                        wait_or_abort(&empty[stage], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY));
         if (!ok) break;
         uint8_t* sw = smem + stage * a.stage_bytes;
         const uint32_t fbar = fbar0 + stage * 8;
@@ -851,15 +866,12 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
             }
           }
         }
-        __syncwarp();  // no lane may fall two phases behind the barrier that it waits on
         ++issued;
         if (++stage == a.stages) {
           stage = 0;
           phase ^= 1u;
         }
       }
-      __syncwarp();
-      ok = __all_sync(0xffffffffu, ok);
     }
     // after an abort, let the copies already issued land before the pair leaves
     if (leader && rank == 0 && *abort_flag)

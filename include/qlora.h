@@ -503,7 +503,7 @@ qlora_status qlora_rmsnorm_mx(const void* X, const void* residual, const void* g
 
 /* qlora_mx_linear_fwd -- Y = x w^T on the block-scaled tensor cores.
  *   x : MX [M, K], either format (from qlora_rmsnorm_mx or qlora_quantize_mx).
- *   w : MX [N, K], QLORA_MX_E2M1 (else UNSUPPORTED).
+ *   w : MX [N, K], QLORA_MX_E2M1, K <= 2^20 (else UNSUPPORTED).
  *   Y : device bf16 [M, N] (16-byte aligned).
  * Products are exact and summed in fp32; Y is rounded once. A NaN block makes its
  * row (of x) or column (of w) of Y NaN. The result does not depend on the other

@@ -256,7 +256,10 @@ def _bits(ref):
 @pytest.mark.parametrize("M,N,K", [(1, 1, 32), (1, 128, 128), (2, 130, 160), (7, 64, 96), (16, 256, 4096), (1, 11008, 512),
                                    (17, 200, 288), (32, 129, 1024), (33, 384, 640), (64, 77, 2080), (65, 512, 256),
                                    (100, 1000, 1056), (128, 128, 4096), (129, 257, 384), (300, 4100, 544),
-                                   (256, 256, 1024), (700, 520, 1184), (1025, 770, 256), (2048, 1024, 512)])
+                                   (256, 256, 1024), (700, 520, 1184), (1025, 770, 256), (2048, 1024, 512),
+                                   # more tiles of 128 x 128 than SMs: CTA pairs, whole and narrow tiles, odd N
+                                   (1200, 2100, 288), (700, 4100, 544), (2049, 1283, 1184), (4096, 1024, 160), (1057, 2560, 96),
+                                   (520, 5000, 2144)])
 def test_product_bits(M, N, K, fmt):
     dev = require_gpu()
     x, xs = _exact_operand(M, K, fmt, 100 + M, 2)
@@ -355,6 +358,12 @@ GROUPS = [
     ([1] * 40, 257, 96),
     ([1000, 3], 513, 384),
     ([5] * 300, 16, 64),
+    # CTA pairs
+    ([602, 30, 87, 67, 134, 14, 39, 27], 1300, 416),
+    ([2000], 1200, 256),
+    ([5, 900, 0, 260], 2051, 160),
+    ([257] * 6, 1281, 1184),
+    ([0] * 40 + [1500] + [33] * 3, 1284, 1056),
 ]
 
 

@@ -124,6 +124,8 @@ def test_refusals_of_the_c_calls():
     assert grp(r, rw, P + 1, 4, P, None) == 3
     assert grp(r, rw, P, 4097, P, None) == 2
     assert grp(r, rw, P, 5, P, None) == 1                       # 64 rows are not 5 experts
+    deep = (1 << 20) + 32
+    assert fwd(ctypes.byref(_mx(cols=deep)), ctypes.byref(_mx(rows=64, cols=deep, fmt=b.MX_E2M1)), P, None) == 2
     many = _mx(rows=(1 << 31) - 1)
     assert fwd(ctypes.byref(many), ctypes.byref(_mx(rows=(1 << 31) - 1, fmt=b.MX_E2M1)), P, None) == 2
     # no rows: nothing to do, and the pointers are not looked at
@@ -213,6 +215,17 @@ def test_refusals_of_the_binding():
         lambda: b.qlora_mx_grouped_fwd(x, w, torch.zeros(1, dtype=torch.int32)),
         lambda: b.qlora_mx_grouped_fwd(x, w, torch.zeros(6, dtype=torch.int32)),
         lambda: b.qlora_mx_grouped_fwd(x, w, torch.zeros(10, dtype=torch.int32)[::2]),
+    ]
+    class OtherStream:
+        device = torch.device("cuda:7")
+
+    other = OtherStream()
+    calls += [  # a stream of another device than the tensors'
+        lambda: b.qlora_quantize_mx(bf(4, 128), b.MX_E4M3, stream=other),
+        lambda: b.qlora_dequantize_mx(x, stream=other),
+        lambda: b.qlora_rmsnorm_mx(bf(4, 128), bf(128), 1e-5, stream=other),
+        lambda: b.qlora_mx_linear_fwd(x, w, stream=other),
+        lambda: b.qlora_mx_grouped_fwd(x, w, torch.zeros(5, dtype=torch.int32), stream=other),
     ]
     for k, call in enumerate(calls):
         with pytest.raises(ValueError):
