@@ -303,6 +303,9 @@ __device__ __forceinline__ void quantize_stages(const MxArgs& a, int64_t row0, i
                                                 volatile int* abort_flag, int32_t* err) {
   using C = MxCfg<TN, DEEP>;
   static_assert(TN == 16, "a lane holds half a token's k-block");
+  // A warp that goes from k-block n - 4 to n has seen n - 4 - STAGES consumed; the parity of n's barrier tells n -
+  // STAGES from n - 2 STAGES only if the latter is among those.
+  static_assert(C::STAGES >= 4, "the parity of a stage's barrier would be ambiguous");
   const int lane = threadIdx.x & 31;
   const int row = lane >> 1, h = lane & 1;
   const bool mine = row < tokens;
@@ -1110,7 +1113,12 @@ static int64_t rows_per_group(int64_t M, int64_t groups) {
   return used > 0 ? (M + used - 1) / used : 0;
 }
 
-bool mx_gemm_quantizes(int64_t M, int64_t groups) { return rows_per_group(M, groups) <= 16; }
+// Most rows of a group, on average, for tiles of 16 tokens: groups are uneven, and a group that needs two tiles reads its
+// weights twice (64 experts, 2048x2048, 500 rows: 42.5 us in tiles of 16, 41.2 of 32; 1000 rows: 58.8 and 44.7; 16
+// experts, 4096x4096, 200 rows: 43.8 and 34.5).
+static int64_t rows_of_16(int64_t groups) { return groups == 1 ? 16 : 8; }
+
+bool mx_gemm_quantizes(int64_t M, int64_t groups) { return rows_per_group(M, groups) <= rows_of_16(groups); }
 
 cudaError_t launch_mx_gemm(const MxView& x, const void* x_bf16, const MxView& w, const int32_t* offsets, int groups,
                            int64_t N, void* Y, int num_sms, int32_t* err, cudaStream_t stream) {
@@ -1132,9 +1140,10 @@ cudaError_t launch_mx_gemm(const MxView& x, const void* x_bf16, const MxView& w,
   // most token tiles that any division of the rows into the groups can need
   const int64_t used = groups < a.M ? groups : a.M;
   auto bound = [&](int tn) { return (a.M + used * (tn - 1)) / tn; };
-  if (per <= 16) return x_bf16 ? run_tiles<16, true>(x, w, a, bound(16), num_sms, err, stream)
-                               : run_tiles<16>(x, w, a, bound(16), num_sms, err, stream);
-  if (per <= 32) return run_tiles<32>(x, w, a, bound(32), num_sms, err, stream);
+  if (per <= rows_of_16(groups))
+    return x_bf16 ? run_tiles<16, true>(x, w, a, bound(16), num_sms, err, stream)
+                  : run_tiles<16>(x, w, a, bound(16), num_sms, err, stream);
+  if (per <= 2 * rows_of_16(groups)) return run_tiles<32>(x, w, a, bound(32), num_sms, err, stream);
   // The narrowest tile that still gives every tile an SM (200 tokens, 4096x4096: 9.6 us in tiles of 64, 10.7 of 128; 333:
   // 13.0 and 11.7), then pairs, whose tiles read less (1024 tokens, 4096x4096: 19.0 us, 18.6 in 256 tiles of 128 tokens;
   // 512, 11008x4096: 27.0 and 33.1).

@@ -541,7 +541,7 @@ qlora_status qlora_mx_grouped_fwd(const qlora_mx_tensor* x, const qlora_mx_tenso
 
 /* qlora_mx_grouped_fwd_bf16 -- qlora_mx_grouped_fwd of bf16 activations, as
  * qlora_mx_linear_fwd_bf16 (the workspace is unused where the groups that can have
- * rows, min(n_groups, M), have 16 or fewer on average). */
+ * rows, min(n_groups, M), have 8 or fewer on average, 16 with one group). */
 qlora_status qlora_mx_grouped_fwd_bf16(const void* X, int64_t M, qlora_mx_format x_format,
                                        const qlora_mx_tensor* w, const int32_t* offsets, int32_t n_groups,
                                        void* Y, void* workspace, size_t* workspace_bytes,

@@ -410,6 +410,28 @@ def test_grouped_with_bad_offsets_stays_in_bounds(off):
     assert torch.all(Y[:4] == 7) and torch.all(Y[4 + M:] == 7)
 
 
+@pytest.mark.parametrize("sizes", [[2, 0, 7, 3, 8], [1] * 30, [40, 0, 0, 1, 2, 0, 1, 1], [9, 20, 3], [16]])
+def test_grouped_from_bf16(sizes):
+    """bf16 activations quantized in the product's kernel or before it: the bits of the two separate calls."""
+    dev = require_gpu()
+    N, K, E, M = 200, 1184, len(sizes), sum(sizes)
+    w = b.qlora_quantize_mx((0.02 * _rand((E * N, K), 2).float()).to(torch.bfloat16).to(dev), b.MX_E2M1)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(sizes)]), dtype=torch.int32, device=dev)
+    X = _rand((M, K), M, spread=3).to(dev)
+    X[0, 40] = float("nan")
+    for fmt in FORMATS:
+        x = b.qlora_quantize_mx(X, fmt)
+        Y, Q = b.qlora_mx_grouped_fwd(X, w, off, x_format=fmt), b.qlora_mx_grouped_fwd(x, w, off)
+        _done()
+        assert torch.isnan(Y[0]).all() and torch.isnan(Q[0]).all()
+        assert torch.equal(Y[1:], Q[1:])
+        xv, wv = _f64(b.qlora_dequantize_mx(x)), _f64(b.qlora_dequantize_mx(w))
+        for e in range(E):
+            a, c = max(1, int(off[e])), int(off[e + 1])
+            if c > a:
+                _check_product(Y[a:c], xv[a:c], wv[e * N:(e + 1) * N])
+
+
 def test_grouped_equals_dense_by_group():
     dev = require_gpu()
     sizes, N, K = [3, 0, 70, 257], 384, 1056
@@ -483,11 +505,13 @@ def test_captured_and_replayed_with_new_inputs():
     off = torch.zeros(E + 1, dtype=torch.int32, device=dev)
     Y = torch.zeros(M, N, dtype=torch.bfloat16, device=dev)
     D = torch.zeros(M, E * N, dtype=torch.bfloat16, device=dev)
+    F = torch.zeros(8, E * N, dtype=torch.bfloat16, device=dev)
 
     def step():
         x, h = b.qlora_rmsnorm_mx(X, g, 1e-5, residual=R)
         b.qlora_mx_grouped_fwd(x, w, off, Y=Y)
-        b.qlora_mx_linear_fwd(h, w, Y=D)
+        b.qlora_mx_linear_fwd(h, w, Y=D)          # quantized into a workspace of the graph
+        b.qlora_mx_linear_fwd(h[:8], w, Y=F)      # quantized in the product's kernel
         return x, h
 
     side = torch.cuda.Stream()
@@ -505,11 +529,11 @@ def test_captured_and_replayed_with_new_inputs():
         Y.fill_(3.0)
         graph.replay()
         _done()
-        gotY, gotD = Y.clone(), D.clone()
+        gotY, gotD, gotF = Y.clone(), D.clone(), F.clone()
         Y.fill_(3.0)
         step()
         _done()
-        assert torch.equal(gotY, Y) and torch.equal(gotD, D)
+        assert torch.equal(gotY, Y) and torch.equal(gotD, D) and torch.equal(gotF, F)
         assert torch.all(Y[sum(sizes):] == 3)
     del graph
 

@@ -151,9 +151,10 @@ def test_refusals_and_workspace_of_the_quantizing_products():
         return n.value
 
     up = lambda v: (v + 255) // 256 * 256  # noqa: E731
-    assert need(0, b.MX_E4M3) == 256 and need(16, b.MX_E4M3) == 256 and need(64, b.MX_E4M3, groups=4) == 256
+    assert need(0, b.MX_E4M3) == 256 and need(16, b.MX_E4M3) == 256 and need(32, b.MX_E4M3, groups=4) == 256
+    assert need(16, b.MX_E4M3, groups=1) == 256
     assert need(17, b.MX_E4M3) == up(17 * 128) + up(17 * 4)
-    assert need(65, b.MX_E2M1, groups=4) == up(65 * 64) + up(65 * 4)
+    assert need(33, b.MX_E2M1, groups=4) == up(33 * 64) + up(33 * 4)
     lin, grp = lib.qlora_mx_linear_fwd_bf16, lib.qlora_mx_grouped_fwd_bf16
     big = 1 << 20
     assert lin(P, 4, 7, rw, P, P, size(big), None) == 2
