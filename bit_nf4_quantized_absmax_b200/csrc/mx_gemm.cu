@@ -16,7 +16,8 @@
 // reads byte j of each word.
 //
 // Two kernels: k_mx_gemm, one tile a CTA or a cluster, for few tokens and for as many
-// tiles as there are SMs; k_mx_gemm_pair, persistent CTA pairs, beyond. Measured on
+// tiles as there are SMs; k_mx_gemm_pair, persistent CTA pairs (for groups of up to 128
+// rows: single CTAs), beyond. Measured on
 // the device (x already MX, weights in rotation over three sets):
 //   one token       4096x4096  5.9 us   11008x4096  7.3 us (24 MB: 3.3 TB/s)
 //   512 tokens      4096x4096 11.8 us   11008x4096 25.9 us
@@ -222,60 +223,70 @@ __device__ __forceinline__ void store_tokens(const uint8_t* stg, __nv_bfloat16* 
   }
 }
 
-// Token tile `want` of the grouped rows, by a whole warp: group e, the tile's first
-// row and the row behind its last. A group of m rows has ceil(m / tn) tiles of equal
-// size, rounded up to a multiple of `unit`. Offsets are read as they are but clamped to
-// [0, M] and to their running maximum, so that no offsets lead outside of x and Y.
+// Token tiles of the grouped rows, found by a whole warp. A group of m rows has
+// ceil(m / tn) tiles of equal size, rounded up to a multiple of `unit`. Offsets are read
+// as they are but clamped to [0, M] and to their running maximum, so that no offsets lead
+// outside of x and Y. Tiles are asked for in ascending order: 32 groups at a time are
+// scanned and kept in the lanes, so that a warp that goes from tile to tile reads and
+// scans each group once (anew for every tile it took 2000 clocks with 64 groups, a fifth
+// of a tile of 16 k-blocks).
 struct TokenTile {
   int group;
   int64_t row0, end;
   bool found;
 };
-__device__ __forceinline__ TokenTile find_token_tile(const int32_t* __restrict__ offsets, int groups, int64_t M,
-                                                     int tn, int unit, int want) {
-  const int lane = threadIdx.x & 31;
-  int64_t carry = 0;  // running maximum of the offsets so far
-  int base = 0;       // tiles before this chunk
-  for (int e0 = 0; e0 < groups; e0 += 32) {
+struct GroupScan {
+  const int32_t* offsets;
+  int groups, M, tn, unit;
+  int e0 = -32;           // first group of the lanes' 32
+  int base = 0, next = 0;  // tiles before them, and before the next 32
+  int carry = 0;          // running maximum of the offsets so far
+  int b = 0, rows = 0, tiles = 0, upto = 0;  // the lane's group: first row, rows, tiles; tiles up to and with it
+  __device__ __forceinline__ GroupScan(const int32_t* offsets_, int groups_, int64_t M_, int tn_, int unit_)
+      : offsets(offsets_), groups(groups_), M(static_cast<int>(M_)), tn(tn_), unit(unit_) {}
+  __device__ __forceinline__ void advance() {
+    const int lane = threadIdx.x & 31;
+    e0 += 32;
+    base = next;
     const int e = e0 + lane;
     const bool in = e < groups;
-    int64_t b = in ? offsets[e] : 0, t = in ? offsets[e + 1] : 0;
-    b = max(b, carry);
+    b = max(in ? offsets[e] : 0, carry);
+    int t = in ? offsets[e + 1] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, b, o);
+      const int v = __shfl_up_sync(0xffffffffu, b, o);
       if (lane >= o) b = max(b, v);
     }
-    t = max(t, b);
+    t = min(max(t, b), M);
     b = min(b, M);
-    t = min(t, M);
-    const int rows = in ? static_cast<int>(t - b) : 0;  // < 2^31
-    const int tiles = rows / tn + (rows % tn != 0);
-    int sum = tiles;
+    rows = in ? t - b : 0;
+    tiles = rows / tn + (rows % tn != 0);
+    upto = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += v;
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
     }
-    const bool mine = in && want >= base + sum - tiles && want < base + sum;
-    const uint32_t hit = __ballot_sync(0xffffffffu, mine);
-    if (hit) {
-      const int src = __ffs(hit) - 1;
-      const int index = want - (base + sum - tiles);
-      const int step = mine ? (rows / tiles + (rows % tiles != 0) + unit - 1) / unit * unit : 0;
-      TokenTile r;
-      r.group = e0 + src;
-      r.row0 = __shfl_sync(0xffffffffu, b + static_cast<int64_t>(index) * step, src);
-      r.end = min(__shfl_sync(0xffffffffu, t, src), r.row0 + __shfl_sync(0xffffffffu, step, src));
-      r.found = true;
-      return r;
-    }
-    base += __shfl_sync(0xffffffffu, sum, 31);
+    upto += base;
+    next = __shfl_sync(0xffffffffu, upto, 31);
     carry = __shfl_sync(0xffffffffu, t, 31);
-    if (!__shfl_sync(0xffffffffu, in ? 1 : 0, 31)) break;
   }
-  return TokenTile{0, 0, 0, false};
-}
+  __device__ __forceinline__ TokenTile find(int want) {
+    while (want >= next && e0 + 32 < groups) advance();
+    TokenTile r{0, 0, 0, false};
+    if (want >= next) return r;
+    const int src = __ffs(__ballot_sync(0xffffffffu, want < upto)) - 1;
+    const int m = __shfl_sync(0xffffffffu, rows, src), n = __shfl_sync(0xffffffffu, tiles, src);
+    const int index = want - (__shfl_sync(0xffffffffu, upto, src) - n);
+    const int step = (m / n + (m % n != 0) + unit - 1) / unit * unit;
+    const int first = __shfl_sync(0xffffffffu, b, src);
+    r.group = e0 + src;
+    r.row0 = static_cast<int64_t>(first) + static_cast<int64_t>(index) * step;
+    r.end = min(static_cast<int64_t>(first) + m, r.row0 + step);
+    r.found = true;
+    return r;
+  }
+};
 
 struct MxArgs {
   const uint4* x_bf16;     // QUANT: activations still to be quantized, [M, K]
@@ -286,6 +297,7 @@ struct MxArgs {
   int64_t M, N, w_rows;
   int n_tiles, nkb, K;
   int stages, stage_bytes;  // pairs: the operands' ring
+  int tile_rows;            // pairs: weight rows a tile
   int tn, step, tok_tiles;  // pairs: most tokens a tile; without groups, tokens of all tiles but the last and their count
   uint32_t idesc;
   bool x_fp4;  // the widening copies of e2m1 count the bytes of codes, not of containers
@@ -424,7 +436,7 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
   const int tok = tile / a.n_tiles;
   const int64_t n0 = static_cast<int64_t>(tile - tok * a.n_tiles) * kMxRows;
   TokenTile tt{0, static_cast<int64_t>(tok) * TN, a.M, true};
-  if (a.offsets) tt = find_token_tile(a.offsets, a.groups, a.M, TN, TN, tok);
+  if (a.offsets) tt = GroupScan(a.offsets, a.groups, a.M, TN, TN).find(tok);
   const int64_t w0 = tt.group * a.N + n0;  // first weight row in w's storage
   const int kb0 = static_cast<int>(static_cast<int64_t>(a.nkb) * rank / S);
   const int kb1 = static_cast<int>(static_cast<int64_t>(a.nkb) * (rank + 1) / S);
@@ -668,6 +680,11 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 // reach the leader's barrier by a release at cluster scope, from a warp that has no
 // loads in flight to wait for: it takes 1000 to 1600 clocks, which bounded the product
 // while there was one in one k-block (1250 clocks a k-block) or in four (410).
+//
+// CG = 1 is the same kernel for single CTAs (128 weight rows by up to 128 tokens), for
+// groups of few rows, where the weights' copies are what counts and have to go on from
+// tile to tile without a pause: two accumulators, and nothing remote (8 groups of 125
+// rows, 4100x4128 each: 45.5 us in pairs, 40.4 so).
 constexpr int kPairMaxStages = 10;
 constexpr int kPairRing = 6 * (kMxRows + 128) * kMxBK;  // bytes of the operands' ring: 6 stages of the widest tile
 constexpr int kPairThreads = 384;  // warps: TMA, MMA (odd CTA: relay), scales of w, scales of x, eight for the epilogue
@@ -675,13 +692,19 @@ constexpr int kPairW = kMxRows * kMxBK;
 constexpr int kPairBatch = 4;      // k-blocks that one elected region issues
 constexpr int kPairSfDepth = 8;    // k-blocks a block of scales
 constexpr int kPairSfSlots = 2;
-constexpr int kPairSfOne = 512 + 1024;  // bytes a k-block: words of 128 weight rows, of 256 tokens
-constexpr int kPairSfSlot = kPairSfDepth * kPairSfOne;
 constexpr int kPairOut = 1024;          // bytes an epilogue warp stages: 16 tokens of 32 weight rows
-constexpr int kPairSmem = kPairRing + kPairSfSlots * kPairSfSlot + 8 * kPairOut + 1024 + 256;
 constexpr uint32_t kPairSfCol = 256;    // first TMEM column of the scales
-constexpr int kPairSfCols = 12;         // columns a k-block
-static_assert(kPairSfCol + kPairSfSlots * kPairSfDepth * kPairSfCols <= 512, "TMEM columns");
+template <int CG>
+struct PairCfg {
+  static constexpr int ROWS = 128 * CG;            // weight rows of a tile
+  static constexpr int SF_ONE = 512 + 512 * CG;    // bytes a k-block: words of 128 weight rows, of 128 CG tokens
+  static constexpr int SF_SLOT = kPairSfDepth * SF_ONE;
+  static constexpr int SF_COLS = 4 + 4 * CG;       // TMEM columns a k-block
+  static constexpr int ACCS = CG == 1 ? 2 : 1;     // accumulators of 128 CG columns
+  static constexpr int EPI_COLS = 64 * CG;         // tokens of an epilogue warp
+  static constexpr int SMEM = kPairRing + kPairSfSlots * SF_SLOT + 8 * kPairOut + 1024 + 256;
+  static_assert(kPairSfCol + kPairSfSlots * kPairSfDepth * SF_COLS <= 512, "TMEM columns");
+};
 
 __device__ __forceinline__ void mma_mx_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
                                             uint32_t sfb, uint32_t acc) {
@@ -717,38 +740,46 @@ struct MxPairTile {
   int width;      // tokens rounded up to 32: the MMA's N
   bool found;
 };
-__device__ __forceinline__ MxPairTile pair_tile(const MxArgs& a, int unit) {
-  const int tok = unit / a.n_tiles;
-  const int64_t row0 = static_cast<int64_t>(tok) * a.step;
-  TokenTile tt{0, row0, min(a.M, row0 + a.step), tok < a.tok_tiles};
-  if (a.offsets) tt = find_token_tile(a.offsets, a.groups, a.M, a.tn, 32, tok);
-  MxPairTile t;
-  t.found = tt.found;
-  t.row0 = tt.row0;
-  t.n0 = static_cast<int64_t>(unit - tok * a.n_tiles) * 256;
-  t.w0 = tt.group * a.N + t.n0;
-  t.rows = static_cast<int>(tt.end - tt.row0);
-  t.width = (t.rows + 31) / 32 * 32;
-  return t;
-}
+// The tiles of a CTA (pair) in turn, for one warp.
+struct PairTiles {
+  const MxArgs& a;
+  GroupScan scan;
+  __device__ __forceinline__ explicit PairTiles(const MxArgs& a_) : a(a_), scan(a_.offsets, a_.groups, a_.M, a_.tn, 32) {}
+  __device__ __forceinline__ MxPairTile operator()(int unit) {
+    const int tok = unit / a.n_tiles;
+    const int64_t row0 = static_cast<int64_t>(tok) * a.step;
+    TokenTile tt{0, row0, min(a.M, row0 + a.step), tok < a.tok_tiles};
+    if (a.offsets) tt = scan.find(tok);
+    MxPairTile t;
+    t.found = tt.found;
+    t.row0 = tt.row0;
+    t.n0 = static_cast<int64_t>(unit - tok * a.n_tiles) * a.tile_rows;
+    t.w0 = tt.group * a.N + t.n0;
+    t.rows = static_cast<int>(tt.end - tt.row0);
+    t.width = (t.rows + 31) / 32 * 32;
+    return t;
+  }
+};
 
-// The scales' side (one warp): GROUPS = 1 this CTA's weight rows, 2 the tile's tokens.
-template <int GROUPS>
+// The scales' side (one warp): this CTA's weight rows (WSIDE) or the tile's tokens.
+template <int CG, bool WSIDE>
 __device__ __forceinline__ void pair_scales(const MxArgs& a, const uint8_t* scales, int64_t rows, int pair, int npairs,
                                             uint32_t rank, uint8_t* dst, uint64_t* sf_full, uint64_t* sf_empty,
                                             volatile int* abort_flag, int32_t* err) {
+  using C = PairCfg<CG>;
   int slot = 0;
   uint32_t phase = 0;
+  PairTiles tile(a);
   for (int unit = pair;; unit += npairs) {
-    const MxPairTile t = pair_tile(a, unit);
+    const MxPairTile t = tile(unit);
     if (!t.found) return;
-    ScaleWords<GROUPS, kPairSfDepth> sc;
-    sc.start(scales, rows, GROUPS == 1 ? t.w0 + rank * 128 : t.row0, GROUPS == 1 ? kMxRows : t.width, 0, a.nkb);
+    ScaleWords<WSIDE ? 1 : CG, kPairSfDepth> sc;
+    sc.start(scales, rows, WSIDE ? t.w0 + rank * 128 : t.row0, WSIDE ? kMxRows : t.width, 0, a.nkb);
     for (int base = 0; base < a.nkb; base += kPairSfDepth) {
       if (!__all_sync(0xffffffffu, wait_or_abort(&sf_empty[slot], phase ^ 1u, abort_flag, err, DEV_TIMEOUT_SMEM_EMPTY)))
         return;
 #pragma unroll
-      for (int i = 0; i < kPairSfDepth; ++i) sc.store(i, dst + slot * kPairSfSlot + i * kPairSfOne);
+      for (int i = 0; i < kPairSfDepth; ++i) sc.store(i, dst + slot * C::SF_SLOT + i * C::SF_ONE);
       fence_async_shared();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(&sf_full[slot]);
@@ -769,7 +800,8 @@ __device__ __forceinline__ void pair_relay(const MxArgs& a, int pair, int npairs
                                            volatile int* abort_flag, int32_t* err) {
   int slot = 0;
   uint32_t phase = 0;
-  for (int unit = pair; pair_tile(a, unit).found; unit += npairs) {
+  PairTiles tile(a);
+  for (int unit = pair; tile(unit).found; unit += npairs) {
     for (int base = 0; base < a.nkb; base += kPairSfDepth) {
       if (!__all_sync(0xffffffffu, wait_or_abort(&sf_full[slot], phase, abort_flag, err, DEV_TIMEOUT_TMA_FULL))) return;
       if ((threadIdx.x & 31) == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&sf_full[slot]), 0));
@@ -782,27 +814,29 @@ __device__ __forceinline__ void pair_relay(const MxArgs& a, int pair, int npairs
   }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+template <int CG>
+__global__ void __launch_bounds__(kPairThreads, 1)
 k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ MxBoxes tm_x, const MxArgs a,
                int32_t* err) {
+  using C = PairCfg<CG>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sf = smem + kPairRing;
-  uint8_t* out = sf + kPairSfSlots * kPairSfSlot;
+  uint8_t* out = sf + kPairSfSlots * C::SF_SLOT;
   uint64_t* full = reinterpret_cast<uint64_t*>(out + 8 * kPairOut);
   uint64_t* empty = full + kPairMaxStages;
   uint64_t* sf_full = empty + kPairMaxStages;
   uint64_t* sf_empty = sf_full + kPairSfSlots;
   uint64_t* accf = sf_empty + kPairSfSlots;
-  uint64_t* acce = accf + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acce + 1);
+  uint64_t* acce = accf + C::ACCS;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acce + C::ACCS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int pair = blockIdx.x >> 1;
-  const int npairs = gridDim.x >> 1;
+  const uint32_t rank = CG == 2 ? cluster_ctarank() : 0u;
+  const int pair = blockIdx.x / CG;
+  const int npairs = gridDim.x / CG;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairMaxStages; ++s) {
@@ -810,44 +844,54 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < kPairSfSlots; ++s) {
-      mbar_init(&sf_full[s], rank == 0 ? 3 : 2);  // the CTA's scale warps; the leader's also the odd CTA's relay
+      mbar_init(&sf_full[s], CG == 2 && rank == 0 ? 3 : 2);  // the CTA's scale warps; the leader's also the odd CTA's relay
       mbar_init(&sf_empty[s], 1);
     }
-    mbar_init(accf, 1);
-    mbar_init(acce, 16);       // both CTAs' epilogue warps
+    for (int s = 0; s < C::ACCS; ++s) {
+      mbar_init(&accf[s], 1);
+      mbar_init(&acce[s], 8 * CG);  // the epilogue warps
+    }
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&tm_w);
     for (int b = 0; b < 4; ++b) prefetch_tmap(&tm_x.m[b]);
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
-                 "r"(512)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    if (CG == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                   "r"(512)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // the peer's barriers are initialised before any remote use
+  if (CG == 2) cluster_sync_all();  // the peer's barriers are initialised before any remote use
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   pdl_enter();
 
   if (warp == 0) {
     // ---------------- TMA (both CTAs; the bytes count on the leader's barrier) ----------------
-    const uint32_t fbar0 = map_to_cta(smem_u32(full), 0);
+    const uint32_t fbar0 = CG == 2 ? map_to_cta(smem_u32(full), 0) : 0u;
     const bool leader = elect_one();
+    PairTiles tile(a);
     int stage = 0;
     uint32_t phase = 0;
     int64_t issued = 0;
     bool ok = true;
     for (int unit = pair; ok; unit += npairs) {
-      const MxPairTile t = pair_tile(a, unit);
+      const MxPairTile t = tile(unit);
       if (!t.found) break;
-      const int half = t.width / 2;
+      const int half = t.width / CG;  // tokens that this CTA stages
       const int32_t wrow = static_cast<int32_t>(t.w0 + rank * 128);
       const int32_t xrow = static_cast<int32_t>(t.row0 + rank * half);
-      const uint32_t bytes = 2 * (kPairW / 2 + half * (a.x_fp4 ? kMxBK / 2 : kMxBK));
+      const uint32_t bytes = CG * (kPairW / 2 + half * (a.x_fp4 ? kMxBK / 2 : kMxBK));
       // The warp stays converged and only the copies are the elected lane's: within `if (elect_one())` around the loop the
       // copies' operands left the uniform registers (tiles of 64 tokens: 8% slower).
       for (int kb = 0; kb < a.nkb && ok; ++kb) {
@@ -859,12 +903,18 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         const uint32_t fbar = fbar0 + stage * 8;
         if (leader) {
           if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
-          tma_load_2d_pair(sw, &tm_w, fbar, kb * kMxBK, wrow);
+          if (CG == 2)
+            tma_load_2d_pair(sw, &tm_w, fbar, kb * kMxBK, wrow);
+          else
+            tma_load_2d(sw, &tm_w, &full[stage], kb * kMxBK, wrow);
           int at = 0;
 #pragma unroll
           for (int b = 0; b < 4; ++b) {  // half = a sum of boxes of 128, 64, 32 and 16 rows
             if (half & (128 >> b)) {
-              tma_load_2d_pair(sw + kPairW + at * kMxBK, &tm_x.m[b], fbar, kb * kMxBK, xrow + at);
+              if (CG == 2)
+                tma_load_2d_pair(sw + kPairW + at * kMxBK, &tm_x.m[b], fbar, kb * kMxBK, xrow + at);
+              else
+                tma_load_2d(sw + kPairW + at * kMxBK, &tm_x.m[b], &full[stage], kb * kMxBK, xrow + at);
               at += 128 >> b;
             }
           }
@@ -882,26 +932,28 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, err, DEV_TIMEOUT_TMA_FULL);
   } else if (warp == 1) {
     // ---------------- MMA (leader CTA), relay (odd CTA) ----------------
-    if (rank == 1) {
+    if (CG == 2 && rank == 1) {
       pair_relay(a, pair, npairs, sf_full, abort_flag, err);
     } else {
       const uint32_t s0 = smem_u32(smem);
       const uint64_t dw0 = smem_desc(s0, 16, 1024), dx0 = smem_desc(s0 + kPairW, 16, 1024);
       const uint64_t df0 = smem_desc_scales(smem_u32(sf));
-      int stage = 0, slot = 0;
+      PairTiles tile(a);
+      int stage = 0, slot = 0, acc = 0;
       uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
       bool ok = true;
       for (int unit = pair; ok; unit += npairs) {
-        const MxPairTile t = pair_tile(a, unit);
+        const MxPairTile t = tile(unit);
         if (!t.found) break;
         const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
         const bool wide = t.width > 128;
-        ok = __all_sync(0xffffffffu, wait_or_abort(acce, acc_phase ^ 1u, abort_flag, err, DEV_TIMEOUT_TMEM_EMPTY));
-        acc_phase ^= 1u;
+        ok = __all_sync(0xffffffffu, wait_or_abort(&acce[acc], acc_phase ^ 1u, abort_flag, err, DEV_TIMEOUT_TMEM_EMPTY));
         tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * 128;
         for (int base = 0; base < a.nkb && ok; base += kPairSfDepth) {
           ok = __all_sync(0xffffffffu,
-                          wait_or_abort_cluster(&sf_full[slot], sf_phase, abort_flag, err, DEV_TIMEOUT_TMA_FULL));
+                          CG == 2 ? wait_or_abort_cluster(&sf_full[slot], sf_phase, abort_flag, err, DEV_TIMEOUT_TMA_FULL)
+                                  : wait_or_abort(&sf_full[slot], sf_phase, abort_flag, err, DEV_TIMEOUT_TMA_FULL));
           if (!ok) break;
           const int end = min(a.nkb, base + kPairSfDepth);
           for (int kb0 = base; kb0 < end && ok; kb0 += kPairBatch) {
@@ -926,22 +978,39 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
                     tc_fence_after();
                     const uint64_t at = static_cast<uint32_t>(st[i] * a.stage_bytes) >> 4;
                     const uint32_t one = slot * kPairSfDepth + (kb0 - base) + i;  // this k-block's place among the scales
-                    const uint64_t df = df0 + one * (kPairSfOne >> 4);
+                    const uint64_t df = df0 + one * (C::SF_ONE >> 4);
                     // TMEM columns of its own: the MMAs that read them last have completed, or the slot would not have
                     // been refilled
-                    const uint32_t tsf = tmem_base + kPairSfCol + kPairSfCols * one;
-                    tmem_copy_scales_pair(tsf, df);
-                    tmem_copy_scales_pair(tsf + 4, df + (512 >> 4));
-                    if (wide) tmem_copy_scales_pair(tsf + 8, df + (1024 >> 4));
+                    const uint32_t tsf = tmem_base + kPairSfCol + C::SF_COLS * one;
+                    if (CG == 2) {
+                      tmem_copy_scales_pair(tsf, df);
+                      tmem_copy_scales_pair(tsf + 4, df + (512 >> 4));
+                      if (wide) tmem_copy_scales_pair(tsf + 8, df + (1024 >> 4));
+                    } else {
+                      tmem_copy_scales(tsf, df);
+                      tmem_copy_scales(tsf + 4, df + (512 >> 4));
+                    }
 #pragma unroll
-                    for (uint32_t j = 0; j < kMxBK / 32; ++j)
-                      mma_mx_pair(tmem_base, dw0 + at + j * 2, dx0 + at + j * 2, idesc | (j << 4) | (j << 29), tsf,
-                                  tsf + 4, (kb0 + i > 0 || j > 0) ? 1u : 0u);
-                    mma_commit_pair(&empty[st[i]]);
+                    for (uint32_t j = 0; j < kMxBK / 32; ++j) {
+                      const uint32_t id = idesc | (j << 4) | (j << 29), more = (kb0 + i > 0 || j > 0) ? 1u : 0u;
+                      if (CG == 2)
+                        mma_mx_pair(d_tmem, dw0 + at + j * 2, dx0 + at + j * 2, id, tsf, tsf + 4, more);
+                      else
+                        mma_mx(d_tmem, dw0 + at + j * 2, dx0 + at + j * 2, id, tsf, tsf + 4, more);
+                    }
+                    if (CG == 2)
+                      mma_commit_pair(&empty[st[i]]);
+                    else
+                      mma_commit(&empty[st[i]]);
                   }
                 }
               }
-              if (good && kb0 + kPairBatch >= end) mma_commit_pair(&sf_empty[slot]);
+              if (good && kb0 + kPairBatch >= end) {
+                if (CG == 2)
+                  mma_commit_pair(&sf_empty[slot]);
+                else
+                  mma_commit(&sf_empty[slot]);
+              }
             }
             __syncwarp();
             ok = __all_sync(0xffffffffu, *abort_flag == 0);
@@ -951,47 +1020,65 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
             sf_phase ^= 1u;
           }
         }
-        if (ok && elect_one()) mma_commit_pair(accf);
+        if (ok && elect_one()) {
+          if (CG == 2)
+            mma_commit_pair(&accf[acc]);
+          else
+            mma_commit(&accf[acc]);
+        }
         __syncwarp();
+        if (++acc == C::ACCS) {
+          acc = 0;
+          acc_phase ^= 1u;
+        }
       }
     }
   } else if (warp < 4) {
     // ---------------- scale words: this CTA's 128 weight rows (warp 2), all tokens of the tile (warp 3) ----------------
     if (warp == 2)
-      pair_scales<1>(a, a.w_scales, a.w_rows, pair, npairs, rank, sf, sf_full, sf_empty, abort_flag, err);
+      pair_scales<CG, true>(a, a.w_scales, a.w_rows, pair, npairs, rank, sf, sf_full, sf_empty, abort_flag, err);
     else
-      pair_scales<2>(a, a.x_scales, a.M, pair, npairs, rank, sf + 512, sf_full, sf_empty, abort_flag, err);
+      pair_scales<CG, false>(a, a.x_scales, a.M, pair, npairs, rank, sf + 512, sf_full, sf_empty, abort_flag, err);
   } else {
-    // ---------------- epilogue: 32 weight rows by 128 tokens a warp ----------------
-    const int quarter = warp & 3, col0 = ((warp - 4) >> 2) * 128;
-    const uint32_t acce_leader = map_to_cta(smem_u32(acce), 0);
+    // ---------------- epilogue: 32 weight rows by EPI_COLS tokens a warp ----------------
+    const int quarter = warp & 3, col0 = ((warp - 4) >> 2) * C::EPI_COLS;
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
     uint8_t* stg = out + (warp - 4) * kPairOut;
+    PairTiles tile(a);
+    int acc = 0;
     uint32_t acc_phase = 0;
     for (int unit = pair;; unit += npairs) {
-      const MxPairTile t = pair_tile(a, unit);
+      const MxPairTile t = tile(unit);
       if (!t.found) break;
-      if (!__all_sync(0xffffffffu, wait_or_abort(accf, acc_phase, abort_flag, err, DEV_TIMEOUT_ACCUM))) break;
-      acc_phase ^= 1u;
+      if (!__all_sync(0xffffffffu, wait_or_abort(&accf[acc], acc_phase, abort_flag, err, DEV_TIMEOUT_ACCUM))) break;
       tc_fence_after();
       // lo, hi: TMEM lanes 0-15 and 16-31, [64 columns][16 of them][fragment]
-      uint32_t lo[2][4][4], hi[2][4][4];
+      uint32_t lo[CG][4][4], hi[CG][4][4];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < CG; ++c) {
         if (col0 + c * 64 < t.width) {  // columns past the width are read but not stored
-          tmem_ld_16x64(tacc + c * 64, lo[c]);
-          tmem_ld_16x64(tacc + (16u << 16) + c * 64, hi[c]);
+          tmem_ld_16x64(tacc + acc * 128 + c * 64, lo[c]);
+          tmem_ld_16x64(tacc + acc * 128 + (16u << 16) + c * 64, hi[c]);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(acce_leader);
+      if (lane == 0) {
+        if (CG == 2)
+          mbar_arrive_cluster_relaxed(map_to_cta(smem_u32(&acce[acc]), 0));
+        else
+          mbar_arrive(&acce[acc]);
+      }
+      if (++acc == C::ACCS) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
       const int64_t n = t.n0 + rank * 128 + quarter * 32;
       const int left = t.rows - col0;
       const int nleft = static_cast<int>(min(static_cast<int64_t>(32), a.N - n));
       __nv_bfloat16* dst = a.Y + (t.row0 + col0) * a.N + n;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
+      for (int c = 0; c < 4 * CG; ++c) {
         if (c * 16 < left && nleft > 0) {
           stage_transposed(stg, lo[c >> 2][c & 3], hi[c >> 2][c & 3]);
           __syncwarp();
@@ -1004,11 +1091,14 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
 
   tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // no CTA leaves while its peer may still signal it
+  if (CG == 2) cluster_sync_all();  // no CTA leaves while its peer may still signal it
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
+    if (CG == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512) : "memory");
   }
 }
 
@@ -1028,16 +1118,14 @@ bool make_mx_map(CUtensorMap* m, const MxView& v, int box_rows) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int TN, bool QUANT, bool DEEP>
-cudaError_t launch_tiles(const CUtensorMap& tw, const CUtensorMap& tx, const MxArgs& a, int64_t tiles, int S,
-                         int32_t* err, cudaStream_t stream) {
-  using C = MxCfg<TN, DEEP>;
-  const cudaError_t e = ensure_smem_limit<k_mx_gemm<TN, QUANT, DEEP>>(C::SMEM);
-  if (e != cudaSuccess) return e;
+// Launch in clusters of S CTAs, after the preceding kernel's trigger.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t ctas, int S, int threads, int smem, cudaStream_t stream,
+                            Args&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
-  cfg.blockDim = dim3(QUANT ? kMxThreads + 128 : kMxThreads);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1048,7 +1136,17 @@ cudaError_t launch_tiles(const CUtensorMap& tw, const CUtensorMap& tx, const MxA
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, k_mx_gemm<TN, QUANT, DEEP>, tw, tx, a, err);
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+template <int TN, bool QUANT, bool DEEP>
+cudaError_t launch_tiles(const CUtensorMap& tw, const CUtensorMap& tx, const MxArgs& a, int64_t tiles, int S,
+                         int32_t* err, cudaStream_t stream) {
+  using C = MxCfg<TN, DEEP>;
+  const cudaError_t e = ensure_smem_limit<k_mx_gemm<TN, QUANT, DEEP>>(C::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_clusters(k_mx_gemm<TN, QUANT, DEEP>, tiles * S, S, QUANT ? kMxThreads + 128 : kMxThreads, C::SMEM,
+                         stream, tw, tx, a, err);
 }
 
 template <int TN, bool QUANT = false>
@@ -1074,9 +1172,11 @@ cudaError_t run_tiles(const MxView& x, const MxView& w, MxArgs a, int64_t tok_ti
   return launch_tiles<TN, QUANT, false>(tw, tx, a, tiles, S, err, stream);
 }
 
-// tn: most tokens a tile, a multiple of 32 up to 256.
+// tn: most tokens a tile, a multiple of 32 up to 128 CG.
+template <int CG>
 cudaError_t run_pairs(const MxView& x, const MxView& w, MxArgs a, int tn, int64_t tok_tiles, int num_sms, int32_t* err,
                       cudaStream_t stream) {
+  using C = PairCfg<CG>;
   CUtensorMap tw;
   MxBoxes tx;
   if (!make_mx_map(&tw, w, kMxRows)) return cudaErrorInvalidValue;
@@ -1085,17 +1185,18 @@ cudaError_t run_pairs(const MxView& x, const MxView& w, MxArgs a, int tn, int64_
   a.tn = tn;
   // A stage's round trip (MMAs done, slot free, copy issued, data there) takes some 2600 clocks, so narrow tiles, whose
   // MMAs are short, use the room that their operands leave for more stages.
-  a.stage_bytes = kPairW + (tn / 2 * kMxBK + 1023) / 1024 * 1024;
+  a.stage_bytes = kPairW + (tn / CG * kMxBK + 1023) / 1024 * 1024;
   a.stages = kPairRing / a.stage_bytes < kPairMaxStages ? kPairRing / a.stage_bytes : kPairMaxStages;
   a.tok_tiles = static_cast<int>(tok_tiles);
   a.step = static_cast<int>(((a.M + tok_tiles - 1) / tok_tiles + 31) / 32 * 32);
-  a.n_tiles = static_cast<int>((a.N + 255) / 256);
-  a.idesc = mx_instr_desc(kFmtE2M1, x.fmt == kMxE2M1 ? kFmtE2M1 : kFmtE4M3, 256, 0);  // N is the tile's
+  a.tile_rows = C::ROWS;
+  a.n_tiles = static_cast<int>((a.N + C::ROWS - 1) / C::ROWS);
+  a.idesc = mx_instr_desc(kFmtE2M1, x.fmt == kMxE2M1 ? kFmtE2M1 : kFmtE4M3, C::ROWS, 0);  // N is the tile's
   const int64_t units = tok_tiles * a.n_tiles;
-  const int pairs = static_cast<int>(units < num_sms / 2 ? units : num_sms / 2);
-  const cudaError_t e = ensure_smem_limit<k_mx_gemm_pair>(kPairSmem);
+  const int pairs = static_cast<int>(units < num_sms / CG ? units : num_sms / CG);
+  const cudaError_t e = ensure_smem_limit<k_mx_gemm_pair<CG>>(C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_mx_gemm_pair, dim3(2 * pairs), dim3(kPairThreads), kPairSmem, stream, tw, tx, a, err);
+  return launch_clusters(k_mx_gemm_pair<CG>, CG * pairs, CG, kPairThreads, C::SMEM, stream, tw, tx, a, err);
 }
 
 }  // namespace
@@ -1144,6 +1245,14 @@ cudaError_t launch_mx_gemm(const MxView& x, const void* x_bf16, const MxView& w,
     return x_bf16 ? run_tiles<16, true>(x, w, a, bound(16), num_sms, err, stream)
                   : run_tiles<16>(x, w, a, bound(16), num_sms, err, stream);
   if (per <= 2 * rows_of_16(groups)) return run_tiles<32>(x, w, a, bound(32), num_sms, err, stream);
+  // Groups of up to 128 rows whose tiles make several rounds of SMs: one CTA per SM that goes from tile to tile, copying
+  // the next one's weights while it finishes. Averages up to 64 rows want many rounds for it (64 groups of 47, 2048x2048:
+  // 42.9 -> 37.9 us; 40 groups of 37: 34.2 and 34.7; 8 groups of 64, 4096x4096: 18.7 and 21.6, tiles of 64 with two CTAs
+  // on an SM); above, it stands against the pairs (8 groups of 125, 4096x4096: 26.6 -> 23.5 us; 8 of 96: 25.7 -> 22.6; of
+  // 187: 28.9 and 37.5).
+  if (offsets && per > 32 && per <= 128 && bound(128) * a.n_tiles > num_sms &&
+      (per > 64 || static_cast<int64_t>(groups) * a.n_tiles > 5 * static_cast<int64_t>(num_sms)))
+    return run_pairs<1>(x, w, a, 128, bound(128), num_sms, err, stream);
   // The narrowest tile that still gives every tile an SM (200 tokens, 4096x4096: 9.6 us in tiles of 64, 10.7 of 128; 333:
   // 13.0 and 11.7), then pairs, whose tiles read less (1024 tokens, 4096x4096: 19.0 us, 18.6 in 256 tiles of 128 tokens;
   // 512, 11008x4096: 27.0 and 33.1).
@@ -1165,7 +1274,7 @@ cudaError_t launch_mx_gemm(const MxView& x, const void* x_bf16, const MxView& w,
       }
     }
   }
-  return run_pairs(x, w, a, tn, bound(tn), num_sms, err, stream);
+  return run_pairs<2>(x, w, a, tn, bound(tn), num_sms, err, stream);
 }
 
 }  // namespace qlora

@@ -364,6 +364,12 @@ GROUPS = [
     ([5, 900, 0, 260], 2051, 160),
     ([257] * 6, 1281, 1184),
     ([0] * 40 + [1500] + [33] * 3, 1284, 1056),
+    ([0] * 33 + [4000, 0, 600], 516, 96),
+    # one CTA from tile to tile
+    ([(i * 37) % 90 for i in range(64)], 1600, 160),
+    ([300, 0, 1, 127, 128, 129], 4100, 1184),
+    ([200 if i % 3 == 0 else i % 7 for i in range(70)], 300, 96),
+    ([0] * 65 + [5500] + [0] * 14 + [1], 130, 1056),
 ]
 
 
