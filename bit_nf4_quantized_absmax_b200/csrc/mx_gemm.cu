@@ -241,7 +241,8 @@ struct GroupScan {
   int e0 = -32;           // first group of the lanes' 32
   int base = 0, next = 0;  // tiles before them, and before the next 32
   int carry = 0;          // running maximum of the offsets so far
-  int b = 0, rows = 0, tiles = 0, upto = 0;  // the lane's group: first row, rows, tiles; tiles up to and with it
+  // the lane's group: first row, row behind its last, tiles, rows of a tile; tiles up to and with it
+  int b = 0, t = 0, tiles = 0, step = 0, upto = 0;
   __device__ __forceinline__ GroupScan(const int32_t* offsets_, int groups_, int64_t M_, int tn_, int unit_)
       : offsets(offsets_), groups(groups_), M(static_cast<int>(M_)), tn(tn_), unit(unit_) {}
   __device__ __forceinline__ void advance() {
@@ -251,7 +252,7 @@ struct GroupScan {
     const int e = e0 + lane;
     const bool in = e < groups;
     b = max(in ? offsets[e] : 0, carry);
-    int t = in ? offsets[e + 1] : 0;
+    t = in ? offsets[e + 1] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, b, o);
@@ -259,8 +260,9 @@ struct GroupScan {
     }
     t = min(max(t, b), M);
     b = min(b, M);
-    rows = in ? t - b : 0;
+    const int rows = in ? t - b : 0;
     tiles = rows / tn + (rows % tn != 0);
+    step = tiles ? (rows / tiles + (rows % tiles != 0) + unit - 1) / unit * unit : 0;
     upto = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -276,13 +278,11 @@ struct GroupScan {
     TokenTile r{0, 0, 0, false};
     if (want >= next) return r;
     const int src = __ffs(__ballot_sync(0xffffffffu, want < upto)) - 1;
-    const int m = __shfl_sync(0xffffffffu, rows, src), n = __shfl_sync(0xffffffffu, tiles, src);
-    const int index = want - (__shfl_sync(0xffffffffu, upto, src) - n);
-    const int step = (m / n + (m % n != 0) + unit - 1) / unit * unit;
-    const int first = __shfl_sync(0xffffffffu, b, src);
+    const int index = want - __shfl_sync(0xffffffffu, upto - tiles, src);
+    const int size = __shfl_sync(0xffffffffu, step, src);
     r.group = e0 + src;
-    r.row0 = static_cast<int64_t>(first) + static_cast<int64_t>(index) * step;
-    r.end = min(static_cast<int64_t>(first) + m, r.row0 + step);
+    r.row0 = static_cast<int64_t>(__shfl_sync(0xffffffffu, b, src)) + static_cast<int64_t>(index) * size;
+    r.end = min(static_cast<int64_t>(__shfl_sync(0xffffffffu, t, src)), r.row0 + size);
     r.found = true;
     return r;
   }
@@ -740,23 +740,36 @@ struct MxPairTile {
   int width;      // tokens rounded up to 32: the MMA's N
   bool found;
 };
-// The tiles of a CTA (pair) in turn, for one warp.
+// The tiles of a CTA (pair) in turn, for one warp: tiles pair, pair + npairs, .. of
+// token tile tok's n_tiles, then the next one's.
 struct PairTiles {
   const MxArgs& a;
   GroupScan scan;
-  __device__ __forceinline__ explicit PairTiles(const MxArgs& a_) : a(a_), scan(a_.offsets, a_.groups, a_.M, a_.tn, 32) {}
-  __device__ __forceinline__ MxPairTile operator()(int unit) {
-    const int tok = unit / a.n_tiles;
+  int tok, part, dtok, dpart;
+  __device__ __forceinline__ PairTiles(const MxArgs& a_, int pair, int npairs)
+      : a(a_), scan(a_.offsets, a_.groups, a_.M, a_.tn, 32) {
+    dtok = npairs / a.n_tiles;
+    dpart = npairs - dtok * a.n_tiles;
+    tok = pair / a.n_tiles;
+    part = pair - tok * a.n_tiles;
+  }
+  __device__ __forceinline__ MxPairTile next() {
     const int64_t row0 = static_cast<int64_t>(tok) * a.step;
     TokenTile tt{0, row0, min(a.M, row0 + a.step), tok < a.tok_tiles};
     if (a.offsets) tt = scan.find(tok);
     MxPairTile t;
     t.found = tt.found;
     t.row0 = tt.row0;
-    t.n0 = static_cast<int64_t>(unit - tok * a.n_tiles) * a.tile_rows;
+    t.n0 = static_cast<int64_t>(part) * a.tile_rows;
     t.w0 = tt.group * a.N + t.n0;
     t.rows = static_cast<int>(tt.end - tt.row0);
     t.width = (t.rows + 31) / 32 * 32;
+    tok += dtok;
+    part += dpart;
+    if (part >= a.n_tiles) {
+      part -= a.n_tiles;
+      ++tok;
+    }
     return t;
   }
 };
@@ -769,9 +782,9 @@ __device__ __forceinline__ void pair_scales(const MxArgs& a, const uint8_t* scal
   using C = PairCfg<CG>;
   int slot = 0;
   uint32_t phase = 0;
-  PairTiles tile(a);
-  for (int unit = pair;; unit += npairs) {
-    const MxPairTile t = tile(unit);
+  PairTiles tiles(a, pair, npairs);
+  while (true) {
+    const MxPairTile t = tiles.next();
     if (!t.found) return;
     ScaleWords<WSIDE ? 1 : CG, kPairSfDepth> sc;
     sc.start(scales, rows, WSIDE ? t.w0 + rank * 128 : t.row0, WSIDE ? kMxRows : t.width, 0, a.nkb);
@@ -800,8 +813,8 @@ __device__ __forceinline__ void pair_relay(const MxArgs& a, int pair, int npairs
                                            volatile int* abort_flag, int32_t* err) {
   int slot = 0;
   uint32_t phase = 0;
-  PairTiles tile(a);
-  for (int unit = pair; tile(unit).found; unit += npairs) {
+  PairTiles tiles(a, pair, npairs);
+  while (tiles.next().found) {
     for (int base = 0; base < a.nkb; base += kPairSfDepth) {
       if (!__all_sync(0xffffffffu, wait_or_abort(&sf_full[slot], phase, abort_flag, err, DEV_TIMEOUT_TMA_FULL))) return;
       if ((threadIdx.x & 31) == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&sf_full[slot]), 0));
@@ -880,13 +893,13 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     // ---------------- TMA (both CTAs; the bytes count on the leader's barrier) ----------------
     const uint32_t fbar0 = CG == 2 ? map_to_cta(smem_u32(full), 0) : 0u;
     const bool leader = elect_one();
-    PairTiles tile(a);
+    PairTiles tiles(a, pair, npairs);
     int stage = 0;
     uint32_t phase = 0;
     int64_t issued = 0;
     bool ok = true;
-    for (int unit = pair; ok; unit += npairs) {
-      const MxPairTile t = tile(unit);
+    while (ok) {
+      const MxPairTile t = tiles.next();
       if (!t.found) break;
       const int half = t.width / CG;  // tokens that this CTA stages
       const int32_t wrow = static_cast<int32_t>(t.w0 + rank * 128);
@@ -938,12 +951,12 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       const uint32_t s0 = smem_u32(smem);
       const uint64_t dw0 = smem_desc(s0, 16, 1024), dx0 = smem_desc(s0 + kPairW, 16, 1024);
       const uint64_t df0 = smem_desc_scales(smem_u32(sf));
-      PairTiles tile(a);
+      PairTiles tiles(a, pair, npairs);
       int stage = 0, slot = 0, acc = 0;
       uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
       bool ok = true;
-      for (int unit = pair; ok; unit += npairs) {
-        const MxPairTile t = tile(unit);
+      while (ok) {
+        const MxPairTile t = tiles.next();
         if (!t.found) break;
         const uint32_t idesc = a.idesc | (static_cast<uint32_t>(t.width >> 3) << 17);
         const bool wide = t.width > 128;
@@ -1044,11 +1057,11 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     const int quarter = warp & 3, col0 = ((warp - 4) >> 2) * C::EPI_COLS;
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
     uint8_t* stg = out + (warp - 4) * kPairOut;
-    PairTiles tile(a);
+    PairTiles tiles(a, pair, npairs);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int unit = pair;; unit += npairs) {
-      const MxPairTile t = tile(unit);
+    while (true) {
+      const MxPairTile t = tiles.next();
       if (!t.found) break;
       if (!__all_sync(0xffffffffu, wait_or_abort(&accf[acc], acc_phase, abort_flag, err, DEV_TIMEOUT_ACCUM))) break;
       tc_fence_after();
@@ -1244,15 +1257,15 @@ cudaError_t launch_mx_gemm(const MxView& x, const void* x_bf16, const MxView& w,
   if (per <= rows_of_16(groups))
     return x_bf16 ? run_tiles<16, true>(x, w, a, bound(16), num_sms, err, stream)
                   : run_tiles<16>(x, w, a, bound(16), num_sms, err, stream);
-  if (per <= 2 * rows_of_16(groups)) return run_tiles<32>(x, w, a, bound(32), num_sms, err, stream);
   // Groups of up to 128 rows whose tiles make several rounds of SMs: one CTA per SM that goes from tile to tile, copying
-  // the next one's weights while it finishes. Averages up to 64 rows want many rounds for it (64 groups of 47, 2048x2048:
-  // 42.9 -> 37.9 us; 40 groups of 37: 34.2 and 34.7; 8 groups of 64, 4096x4096: 18.7 and 21.6, tiles of 64 with two CTAs
-  // on an SM); above, it stands against the pairs (8 groups of 125, 4096x4096: 26.6 -> 23.5 us; 8 of 96: 25.7 -> 22.6; of
-  // 187: 28.9 and 37.5).
-  if (offsets && per > 32 && per <= 128 && bound(128) * a.n_tiles > num_sms &&
+  // the next one's weights while it finishes. Averages of 16 to 64 rows want many rounds for it (256 groups of 16,
+  // 2048x512: 124 -> 87 us; 128 of 23, 768x2048: 43.8 -> 40.6; 64 of 47, 2048x2048: 55.6 -> 47.9; but 128 of 12,
+  // 768x2048: 35.7 and 38.5; 8 of 64, 4096x4096, in two rounds: 18.7 and 21.6), larger ones do not (8 of 125, 4096x4096:
+  // 26.6 -> 23.5 us, in pairs before; 8 of 187: 28.9 and 37.5).
+  if (offsets && per >= 16 && per <= 128 && bound(128) * a.n_tiles > num_sms &&
       (per > 64 || static_cast<int64_t>(groups) * a.n_tiles > 5 * static_cast<int64_t>(num_sms)))
     return run_pairs<1>(x, w, a, 128, bound(128), num_sms, err, stream);
+  if (per <= 2 * rows_of_16(groups)) return run_tiles<32>(x, w, a, bound(32), num_sms, err, stream);
   // The narrowest tile that still gives every tile an SM (200 tokens, 4096x4096: 9.6 us in tiles of 64, 10.7 of 128; 333:
   // 13.0 and 11.7), then pairs, whose tiles read less (1024 tokens, 4096x4096: 19.0 us, 18.6 in 256 tiles of 128 tokens;
   // 512, 11008x4096: 27.0 and 33.1).

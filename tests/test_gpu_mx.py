@@ -370,6 +370,7 @@ GROUPS = [
     ([300, 0, 1, 127, 128, 129], 4100, 1184),
     ([200 if i % 3 == 0 else i % 7 for i in range(70)], 300, 96),
     ([0] * 65 + [5500] + [0] * 14 + [1], 130, 1056),
+    ([17, 0, 40, 9] * 64, 400, 64),
 ]
 
 
