@@ -195,6 +195,17 @@ __device__ __forceinline__ void rsqrt_head_tail(double v, float& hi, float& lo) 
   if (!(fabsf(hi) < __int_as_float(0x7F800000))) lo = 0.0f;  // infinite or NaN
 }
 
+// a * b + c rounded toward zero
+__device__ __forceinline__ f32x2 fma_rz_f32x2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rz.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // h = bf16(x + residual) (or x), rstd = 1 / sqrt(mean(h^2) + eps), y = h rstd
 // gamma, y to MX blocks: a CTA a row, the row read once and kept in registers
 // (8 elements a chunk, CHUNKS chunks a thread), so x and the residual cross
@@ -204,7 +215,11 @@ __device__ __forceinline__ void rsqrt_head_tail(double v, float& hi, float& lo) 
 // The squares of bf16 values are exact in fp32; a thread adds at most 16 + 16 of
 // them in fp32 and the rest of the sum, the mean and rstd are fp64 (a few operations
 // a warp). h * gamma is exact in fp32 too, and rstd enters as a head and a tail,
-// so y carries one fp32 rounding before it is quantized. Four neighbouring
+// so y carries one fp32 rounding. It is a rounding to odd (toward zero, then the last bit
+// set), since a y that became a tie of the element type only by its rounding would be
+// rounded a second time, to even (8 of 16 million e4m3 elements). rstd is a power of two
+// or no binary fraction at all, so y is exact, and the bit stays, for the power alone; a
+// zero becomes 2^-149, which is a zero again under every scale. Four neighbouring
 // lanes hold a block; the sixteen lanes of 128 elements make a scale word.
 template <int FMT, int CHUNKS, bool RES>
 __global__ void __launch_bounds__(1024)
@@ -271,6 +286,7 @@ k_rmsnorm_mx(const uint4* __restrict__ X, const uint4* residual, const uint4* __
     for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);  // the same order in every warp
     float r_hi, r_lo;
     rsqrt_head_tail(d * inv_cols + static_cast<double>(eps), r_hi, r_lo);
+    const uint32_t odd = r_lo == 0.0f && (__float_as_uint(r_hi) << 9) == 0 ? 0u : 1u;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
       const int i = c * T + threadIdx.x;
@@ -282,7 +298,9 @@ k_rmsnorm_mx(const uint4* __restrict__ X, const uint4* residual, const uint4* __
       for (int j = 0; j < 4; ++j) {
         const f32x2 a = mul_f32x2({bf16lo_to_f32(h[c][j]), bf16hi_to_f32(h[c][j])},
                                   {bf16lo_to_f32(gg[j]), bf16hi_to_f32(gg[j])});
-        y[j] = fma_f32x2(a, {r_hi, r_hi}, mul_f32x2(a, {r_lo, r_lo}));
+        y[j] = fma_rz_f32x2(a, {r_hi, r_hi}, mul_f32x2(a, {r_lo, r_lo}));
+        y[j].x = __uint_as_float(__float_as_uint(y[j].x) | odd);
+        y[j].y = __uint_as_float(__float_as_uint(y[j].y) | odd);
         big = max_nan(big, max_nan(fabsf(y[j].x), fabsf(y[j].y)));
       }
       uint32_t m = __float_as_uint(big);

@@ -202,6 +202,54 @@ def test_rmsnorm(shape, residual, fmt):
         assert torch.all(s[-1, :, (shape[1] % 128) // 32:] == 127)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rmsnorm_is_not_rounded_twice(fmt):
+    """The squares of whole numbers up to 255 add up exactly in a thread's fp32, so rstd is good to 2^-40 and every code is that of the
+    exact y: an fp32 y that is a tie of the element type only by its own rounding does not decide for the even one."""
+    dev = require_gpu()
+    shape = (4096, 4096)
+    gen = torch.Generator().manual_seed(77)
+    X = torch.randint(-255, 256, shape, generator=gen).to(torch.bfloat16)
+    g = (1 + torch.rand(shape[1], generator=gen)).to(torch.bfloat16)
+    q, _ = b.qlora_rmsnorm_mx(X.to(dev), g.to(dev), 1e-5, fmt)
+    _done()
+    y = mx.rmsnorm(_f64(X), _f64(g), float(np.float32(1e-5)))
+    codes, sc = mx.unpack(q.data.cpu().numpy(), q.scales.cpu().numpy(), *shape, fmt)
+    near = []
+    for sign in (-1, 1):  # what values 2^-38 off would give: no statement where they differ
+        near.append(mx.quantize(y * (1 + sign * 2.0 ** -38), fmt))
+    sure = (near[0][0] == near[1][0])
+    assert np.array_equal(sc, near[0][1]) and np.array_equal(sc, near[1][1])
+    assert sure.mean() > 0.9999
+    bad = (codes != near[0][0]) & sure
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rmsnorm_exact_ties_and_zeros(fmt):
+    """Where rstd is a power of two, y is exact and its ties go to even; zeros stay zeros, alone in a block or among
+    others."""
+    dev = require_gpu()
+    X = torch.full((4, 1024), 4.0, dtype=torch.bfloat16)
+    X[1] = -0.5
+    X[2, 1::2] = 0          # the mean of the squares is 8: rstd is no binary fraction
+    X[2, 64:128] = 0
+    X[3] = 0
+    g = ((torch.arange(1024) % 256 + 1).float() / 64).to(torch.bfloat16)
+    for e in (0.0, 2.0 ** -40):
+        rows = 3 if e == 0.0 else 4
+        q, _ = b.qlora_rmsnorm_mx(X[:rows].to(dev), g.to(dev), e, fmt)
+        _done()
+        y = mx.rmsnorm(_f64(X[:rows]), _f64(g), e)
+        codes, sc = mx.unpack(q.data.cpu().numpy(), q.scales.cpu().numpy(), rows, 1024, fmt)
+        want, scales = mx.quantize(y, fmt)
+        exact = [0, 1] if e == 0.0 else [3]
+        assert np.array_equal(sc[exact], scales[exact])
+        v, w = mx.decode(codes, fmt), mx.decode(want, fmt)
+        assert np.array_equal(v[exact], w[exact])
+        assert np.array_equal(v[2] == 0, w[2] == 0) and not v[2, 64:128].any()
+
+
 def test_rmsnorm_in_place_and_edges():
     dev = require_gpu()
     X, R = _rand((6, 256), 21), _rand((6, 256), 22)
