@@ -593,6 +593,60 @@ def test_captured_and_replayed_with_new_inputs():
     del graph
 
 
+def test_persistent_tiles_on_two_streams_and_replayed():
+    """Grids of one CTA (or pair) per SM, twice at once, and in a graph whose offsets change between replays, to ones
+    that leave most CTAs without a tile too."""
+    dev = require_gpu()
+    M, N, K, E = 900, 2600, 288, 8
+    W = (0.02 * _rand((E * N, K), 2).float()).to(torch.bfloat16).to(dev)
+    X, X2 = _rand((M, K), 3).to(dev), _rand((3 * M, K), 4).to(dev)
+    w = b.qlora_quantize_mx(W, b.MX_E2M1)
+    x = b.qlora_quantize_mx(X, b.MX_E4M3)    # 113 rows a group: single CTAs
+    x2 = b.qlora_quantize_mx(X2, b.MX_E4M3)  # 338: pairs
+    cuts = [[100, 100, 100, 100, 200, 100, 100, 100], [900, 0, 0, 0, 0, 0, 0, 0], [0] * 8, [1, 0, 500, 3, 0, 0, 0, 300]]
+    offs = [torch.tensor(np.concatenate([[0], np.cumsum(c)]), dtype=torch.int32, device=dev) for c in cuts]
+    fill = lambda m: torch.full((m, N), 5.0, dtype=torch.bfloat16, device=dev)  # noqa: E731
+    want = []
+    for off, c in zip(offs, cuts):
+        y, y2 = fill(M), fill(3 * M)
+        for e in range(E):  # the dense product of the group's rows: other tiles and orders of the sum
+            r = slice(int(off[e]), int(off[e + 1]))
+            if c[e]:
+                we = b.qlora_quantize_mx(W[e * N:(e + 1) * N], b.MX_E2M1)
+                y[r] = b.qlora_mx_linear_fwd(b.qlora_quantize_mx(X[r], b.MX_E4M3), we)
+                y2[r] = b.qlora_mx_linear_fwd(b.qlora_quantize_mx(X2[r], b.MX_E4M3), we)
+        want.append((y, y2))
+    _done()
+    # the fp32 sums of 288 terms, sum of magnitudes under 12, differ by at most 2 * 288 * 2^-24 * 12; a step of bf16 more
+    close = lambda a, c: torch.allclose(a.float(), c.float(), rtol=2.0 ** -7, atol=576 * 12 * 2.0 ** -24)  # noqa: E731
+    got = []
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for off in offs:
+        ys = fill(M), fill(3 * M), fill(M), fill(3 * M)
+        torch.cuda.synchronize()
+        for s, (p, p2) in ((s1, ys[:2]), (s2, ys[2:])):
+            b.qlora_mx_grouped_fwd(x, w, off, Y=p, stream=s)
+            b.qlora_mx_grouped_fwd(x2, w, off, Y=p2, stream=s)
+        _done()
+        assert torch.equal(ys[0], ys[2]) and torch.equal(ys[1], ys[3])
+        got.append(ys[:2])
+    for (a, a2), (c, c2) in zip(got, want):
+        assert close(a, c) and close(a2, c2)
+    off, y, y2 = offs[0].clone(), fill(M), fill(3 * M)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.qlora_mx_grouped_fwd(x, w, off, Y=y)
+        b.qlora_mx_grouped_fwd(x2, w, off, Y=y2)
+    for o, (a, a2) in zip(offs, got):
+        off.copy_(o)
+        y.fill_(5.0)
+        y2.fill_(5.0)
+        graph.replay()
+        _done()
+        assert torch.equal(y, a) and torch.equal(y2, a2)
+    del graph
+
+
 def test_empty_calls():
     dev = require_gpu()
     w = b.qlora_quantize_mx(torch.zeros(64, 64, dtype=torch.bfloat16, device=dev), b.MX_E2M1)
