@@ -494,7 +494,9 @@ qlora_status qlora_dequantize_mx(const qlora_mx_tensor* q, void* out_bf16, qlora
  *                  in place). Required with a residual, ignored without one.
  *   gamma        : device bf16 [q->cols].   eps >= 0.
  * The mean and the root are evaluated in fp64 from fp32 partial sums of at most 32
- * squares (which overflow for |h| above about 10^18), y carries one fp32 rounding.
+ * squares (which overflow for |h| above about 10^18 and vanish below 10^-22), h * gamma
+ * in fp32, exact within its range (infinite above it), and y is rounded to odd in fp32,
+ * so that its code is that of the unrounded y.
  * A row that holds an infinity or a NaN, or only zeros with eps == 0, quantizes to
  * NaN where its y is not finite. rows == 0 writes nothing.
  * Errors: INVALID_ARG (also eps < 0 or NaN), UNSUPPORTED, ALIGNMENT, CUDA, DEVICE. */
