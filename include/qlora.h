@@ -493,10 +493,10 @@ qlora_status qlora_dequantize_mx(const qlora_mx_tensor* q, void* out_bf16, qlora
  *   residual_out : device bf16 of X's shape; may be `residual` itself (an update
  *                  in place). Required with a residual, ignored without one.
  *   gamma        : device bf16 [q->cols].   eps >= 0.
- * The mean and the root are evaluated in fp64 from fp32 partial sums of at most 32
- * squares (which overflow for |h| above about 10^18 and vanish below 10^-22), h * gamma
- * in fp32, exact within its range (infinite above it), and y is rounded to odd in fp32,
- * so that its code is that of the unrounded y.
+ * The squares, their mean and the root are evaluated in fp64, 1 / root is held in fp32 as a
+ * head and a tail (for roots of about 10^-37 to 10^31), h * gamma in fp32, exact within its
+ * range (infinite above it), and y is rounded to odd in fp32, so that its code is that of
+ * the unrounded y, known to within 2^-42.
  * A row that holds an infinity or a NaN, or only zeros with eps == 0, quantizes to
  * NaN where its y is not finite. rows == 0 writes nothing.
  * Errors: INVALID_ARG (also eps < 0 or NaN), UNSUPPORTED, ALIGNMENT, CUDA, DEVICE. */

@@ -225,6 +225,46 @@ def test_rmsnorm_is_not_rounded_twice(fmt):
     assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4])
 
 
+# The squares are added up in fp64 (some 45 additions one after another: 2^-47), the root is a 2-ulp fp32 estimate, within
+# 2^-22, after one Newton step (1.5 * 2^-44), and its head and tail hold 48 bits: y is known to within 2^-43.
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("shape", [(1500, 288), (2000, 4096), (517, 5152), (300, 16416)])
+def test_rmsnorm_codes_of_the_exact_value(shape, residual, fmt):
+    """Rows of any bf16 numbers: every code is that of the exact y, wherever it is one for all y within 2^-42. (Partial sums in
+    fp32 would leave 2 or 3 codes of 16 million off.)"""
+    dev = require_gpu()
+    X, R = _rand(shape, 31, spread=3), _rand(shape, 32, spread=3)
+    g = (1 + 0.1 * _rand((shape[1],), 33).float()).to(torch.bfloat16)
+    q, _ = b.qlora_rmsnorm_mx(X.to(dev), g.to(dev), 1e-5, fmt, residual=R.to(dev) if residual else None)
+    _done()
+    h = (X.float() + R.float()).to(torch.bfloat16) if residual else X
+    y = mx.rmsnorm(_f64(h), _f64(g), float(np.float32(1e-5)))
+    codes, sc = mx.unpack(q.data.cpu().numpy(), q.scales.cpu().numpy(), *shape, fmt)
+    (c0, s0), (c1, s1) = (mx.quantize(y * (1 + sign * 2.0 ** -42), fmt) for sign in (-1, 1))
+    sure, sure_scale = c0 == c1, s0 == s1
+    assert sure.mean() > 0.99999 and sure_scale.all()
+    assert np.array_equal(sc, s0)
+    bad = (codes != c0) & sure
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rmsnorm_of_large_and_small_rows(fmt):
+    """Scaled by a power of two, with eps = 0, a row has the codes of the row itself: the squares overflow or vanish in fp32,
+    not in fp64."""
+    dev = require_gpu()
+    X = _rand((40, 4128), 34)
+    g = (1 + 0.1 * _rand((4128,), 35).float()).to(torch.bfloat16)
+    q, _ = b.qlora_rmsnorm_mx(X.to(dev), g.to(dev), 0.0, fmt)
+    for e in (-110, -75, 66, 100):
+        Xs = torch.ldexp(X.float(), torch.tensor(e)).to(torch.bfloat16)
+        assert torch.equal(torch.ldexp(Xs.double(), torch.tensor(-e)), X.double())
+        t, _ = b.qlora_rmsnorm_mx(Xs.to(dev), g.to(dev), 0.0, fmt)
+        _done()
+        assert torch.equal(q.scales, t.scales) and torch.equal(q.data, t.data), e
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_rmsnorm_exact_ties_and_zeros(fmt):
     """Where rstd is a power of two, y is exact and its ties go to even; zeros stay zeros, alone in a block or among
