@@ -215,12 +215,19 @@ __device__ __forceinline__ f32x2 fma_rz_f32x2(f32x2 a, f32x2 b, f32x2 c) {
 // Squares, their sum, the mean and rstd are fp64: with the 16 + 16 squares of a thread
 // added up in fp32, 2 or 3 of 16 million e4m3 codes were not those of the exact y (4096x4096
 // with a residual 22.6 us either way; e2m1 without one 15.4 us then, 16.6 so). h * gamma is
-// exact in fp32, and rstd enters as a head and a tail, so y carries one fp32 rounding. It is a rounding to odd (toward zero, then the last bit
-// set), since a y that became a tie of the element type only by its rounding would be
-// rounded a second time, to even (8 of 16 million e4m3 elements). rstd is a power of two
-// or no binary fraction at all, so y is exact, and the bit stays, for the power alone; a
-// zero becomes 2^-149, which is a zero again under every scale. Four neighbouring
-// lanes hold a block; the sixteen lanes of 128 elements make a scale word.
+// exact in fp32, and rstd enters as a head and a tail, so y carries one fp32 rounding. It is
+// a rounding to odd (toward zero, then the last bit set), since a y that became a tie of the
+// element type only by its rounding would be rounded a second time, to even (8 of 16 million
+// e4m3 elements).
+//
+// Where rstd is itself a binary fraction p / 2^k, p odd, y is exact and may be a true tie,
+// so the bit stays. Then t = sum(h^2) + eps cols, a binary fraction too, has t p^2 =
+// cols 4^k, so p^2 divides the odd part of cols: p <= 31, since cols is a multiple of 32 up
+// to 32768. Such an rstd is found by its five leading bits and rstd^2 t = cols, whose left
+// side is exact up to its last rounding; h gamma rstd then has 21 bits at most.
+//
+// A zero becomes 2^-149, which is a zero again under every scale. Four neighbouring lanes
+// hold a block; the sixteen lanes of 128 elements make a scale word.
 template <int FMT, int CHUNKS, bool RES>
 __global__ void __launch_bounds__(1024)
 k_rmsnorm_mx(const uint4* __restrict__ X, const uint4* residual, const uint4* __restrict__ gamma, float eps,
@@ -230,7 +237,7 @@ k_rmsnorm_mx(const uint4* __restrict__ X, const uint4* residual, const uint4* __
   const int kp = (cols + 127) / 128 * 128;
   const int nchunk = cols / 8, nchunk_p = kp / 8;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const double inv_cols = 1.0 / cols;
+  const double inv_cols = 1.0 / cols, eps_cols = static_cast<double>(eps) * cols;
   pdl_enter();
   uint4 xq[CHUNKS], rq[CHUNKS], gq[CHUNKS];
   auto load = [&](int64_t row) {
@@ -285,8 +292,12 @@ k_rmsnorm_mx(const uint4* __restrict__ X, const uint4* residual, const uint4* __
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);  // the same order in every warp
     float r_hi, r_lo;
-    rsqrt_head_tail(d * inv_cols + static_cast<double>(eps), r_hi, r_lo);
-    const uint32_t odd = r_lo == 0.0f && (__float_as_uint(r_hi) << 9) == 0 ? 0u : 1u;
+    const double t = d + eps_cols;
+    rsqrt_head_tail(t * inv_cols, r_hi, r_lo);
+    const bool fraction = (__float_as_uint(r_hi) & 0x7FFFFu) == 0u &&
+                          static_cast<double>(r_hi) * static_cast<double>(r_hi) * t == static_cast<double>(cols);
+    if (fraction) r_lo = 0.0f;
+    const uint32_t odd = fraction ? 0u : 1u;
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
       const int i = c * T + threadIdx.x;

@@ -496,7 +496,8 @@ qlora_status qlora_dequantize_mx(const qlora_mx_tensor* q, void* out_bf16, qlora
  * The squares, their mean and the root are evaluated in fp64, 1 / root is held in fp32 as a
  * head and a tail (for roots of about 10^-37 to 10^31), h * gamma in fp32, exact within its
  * range (infinite above it), and y is rounded to odd in fp32, so that its code is that of
- * the unrounded y, known to within 2^-42.
+ * the unrounded y, known to within 2^-42. Where 1 / root is a binary fraction, y is exact and
+ * its ties go to even.
  * A row that holds an infinity or a NaN, or only zeros with eps == 0, quantizes to
  * NaN where its y is not finite. rows == 0 writes nothing.
  * Errors: INVALID_ARG (also eps < 0 or NaN), UNSUPPORTED, ALIGNMENT, CUDA, DEVICE. */

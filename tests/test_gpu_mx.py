@@ -290,6 +290,38 @@ def test_rmsnorm_exact_ties_and_zeros(fmt):
         assert np.array_equal(v[2] == 0, w[2] == 0) and not v[2, 64:128].any()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("cols,ones,eps,p,k", [
+    (288, 128, 0.0, 3, 1), (288, 92, 0.125, 3, 1), (800, 512, 0.0, 5, 2), (1568, 128, 0.0, 7, 1), (9248, 2048, 0.0, 17, 3),
+    (30752, 8192, 0.0, 31, 4), (1024, 256, 0.0, 1, -1)])
+def test_rmsnorm_ties_where_rstd_is_a_fraction(cols, ones, eps, p, k, fmt):
+    """rstd = p / 2^k exactly, which column counts with an odd square factor allow: y is exact and its ties go to even. With
+    one more, tiny element rstd is just below it, and no y is a tie any longer."""
+    dev = require_gpu()
+    rstd = p / 2.0 ** k
+    assert (ones + eps * cols) * rstd * rstd == cols
+    X = torch.zeros(3, cols, dtype=torch.bfloat16)
+    X[:, :ones] = 1.0
+    X[1] *= -1
+    X[2, -1] = 2.0 ** -11 if ones < cols - 32 else 0.0
+    g = torch.ones(cols, dtype=torch.bfloat16)
+    g[:ones] = (torch.arange(ones) % 256 + 1).float().to(torch.bfloat16)  # y: odd multiples of p / 2^k among them
+    q, _ = b.qlora_rmsnorm_mx(X.to(dev), g.to(dev), eps, fmt)
+    _done()
+    codes, sc = mx.unpack(q.data.cpu().numpy(), q.scales.cpu().numpy(), 3, cols, fmt)
+    exact = np.stack([_f64(X[i]) * _f64(g) * rstd for i in (0, 1)])
+    want, scales = mx.quantize(exact, fmt)
+    assert np.array_equal(sc[:2], scales)
+    assert np.array_equal(mx.decode(codes[:2], fmt), mx.decode(want, fmt))
+    table = mx.MAGNITUDES[fmt]
+    u = np.abs(np.ldexp(exact.reshape(2, -1, 32), 127 - scales.astype(np.int64)[..., None]))
+    # There are ties where they can be: a midpoint is an odd number of 5 (e4m3) or 3 bits (e2m1) times a power of two, and a
+    # multiple of p is such a number for p up to 31 or 7 alone.
+    assert np.isin(u, (table[:-1] + table[1:]) / 2).any() == (p <= (31 if fmt == b.MX_E4M3 else 7))
+    below, bscale = mx.quantize(mx.rmsnorm(_f64(X[2:]), _f64(g), eps), fmt)  # 2^-22 / (2 * 8192) below at least: 2^-36
+    assert np.array_equal(sc[2:], bscale) and np.array_equal(mx.decode(codes[2:], fmt), mx.decode(below, fmt))
+
+
 def test_rmsnorm_in_place_and_edges():
     dev = require_gpu()
     X, R = _rand((6, 256), 21), _rand((6, 256), 22)
