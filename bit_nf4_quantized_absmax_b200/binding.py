@@ -496,7 +496,7 @@ class MXTensor:
     MX_E2M1); the layout of `data` and `scales` is that of qlora_mx_tensor in
     include/qlora.h. Made from two contiguous uint8 tensors of the stated sizes in
     any shape, or with MXTensor.empty, which allocates both at once."""
-    __slots__ = ("_data", "_scales", "rows", "cols", "format", "device", "_c")
+    __slots__ = ("_buf", "_data", "_scales", "rows", "cols", "format", "device", "_c")
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, rows: int, cols: int, format: int):
         nd, ns = _mx_bytes(rows, cols, format)
@@ -508,6 +508,7 @@ class MXTensor:
             raise ValueError(f"data and scales of {data.numel()} and {scales.numel()} bytes do not hold "
                              f"[{rows}, {cols}] ({nd} and {ns} bytes)")
         self._data, self._scales, self.rows, self.cols, self.format, self.device = data, scales, rows, cols, format, device
+        self._buf = None
         self._c = _MX(data.data_ptr(), scales.data_ptr(), rows, cols, format)
 
     def as_c(self) -> _MX:
@@ -528,18 +529,21 @@ class MXTensor:
         return self._scales
 
     def _split(self):
-        buf = self._data
+        """Views of the one buffer. Threads may be here together: the buffer stays, and `_scales`, which says that
+        both views are there, is set last."""
         nd, _ = _mx_bytes(self.rows, self.cols, self.format)
         kp = (self.cols + 127) // 128 * 128
-        self._data = buf[:nd].view(self.rows, kp // 2 if self.format == MX_E2M1 else kp)
-        self._scales = buf[nd:].view(kp // 128, self.rows, 4)
+        data = self._buf[:nd].view(self.rows, kp // 2 if self.format == MX_E2M1 else kp)
+        scales = self._buf[nd:].view(kp // 128, self.rows, 4)
+        self._data = data
+        self._scales = scales
 
     @staticmethod
     def empty(rows: int, cols: int, format: int, device="cuda") -> "MXTensor":
         nd, ns = _mx_bytes(rows, cols, format)  # nd is a multiple of 64
         buf = torch.empty(nd + ns, dtype=_U8, device=device)
         q = MXTensor.__new__(MXTensor)
-        q._data, q._scales, q.rows, q.cols, q.format, q.device = buf, None, rows, cols, format, buf.device
+        q._buf, q._scales, q.rows, q.cols, q.format, q.device = buf, None, rows, cols, format, buf.device
         p = buf.data_ptr()
         q._c = _MX(p, p + nd, rows, cols, format)
         return q

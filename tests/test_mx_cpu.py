@@ -3,6 +3,8 @@ and every refusal of the C entry points and of the binding. Nothing is launched.
 from __future__ import annotations
 
 import ctypes
+import sys
+import threading
 
 import numpy as np
 import pytest
@@ -232,3 +234,31 @@ def test_refusals_of_the_binding():
         with pytest.raises(ValueError):
             call()
             pytest.fail(f"call {k} was not refused")
+
+
+def test_storage_views_asked_for_by_several_threads():
+    """`data` and `scales` of a result are views that the first access makes; any thread may be that one."""
+    failures = []
+
+    def look(q, at, start):
+        start.wait()
+        try:
+            assert q.data.shape == (2, 128) and q.scales.shape == (1, 2, 4)
+            assert q.data.data_ptr() == at and q.scales.data_ptr() == at + 256
+        except BaseException as e:  # noqa: BLE001
+            failures.append(repr(e))
+
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        for _ in range(400):
+            q = _tensors(2, 32, b.MX_E4M3)
+            start = threading.Barrier(4)
+            threads = [threading.Thread(target=look, args=(q, q.as_c().data, start)) for _ in range(4)]
+            for t in threads:
+                t.start()
+            for t in threads:
+                t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    assert not failures, (len(failures), failures[0])
