@@ -262,3 +262,126 @@ def test_storage_views_asked_for_by_several_threads():
     finally:
         sys.setswitchinterval(interval)
     assert not failures, (len(failures), failures[0])
+
+
+class _Reached(Exception):
+    """A call got past the binding's checks."""
+
+
+def _bf(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def _offsets(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+class _StreamOfAnotherDevice:
+    device = torch.device("cuda:7")
+
+
+def _accepted():
+    """Calls that pass every check of the binding but that of the device's type."""
+    w, x = _tensors(64, 128, b.MX_E2M1), _tensors(4, 128, b.MX_E4M3)
+    return {
+        "quantize": lambda **k: b.qlora_quantize_mx(**{"X": _bf(4, 128), "format": b.MX_E4M3, **k}),
+        "dequantize": lambda **k: b.qlora_dequantize_mx(**{"q": x, **k}),
+        "norm": lambda **k: b.qlora_rmsnorm_mx(**{"X": _bf(4, 128), "gamma": _bf(128), "eps": 1e-5, **k}),
+        "linear": lambda **k: b.qlora_mx_linear_fwd(**{"x": x, "w": w, **k}),
+        "grouped": lambda **k: b.qlora_mx_grouped_fwd(**{"x": x, "w": w, "offsets": _offsets(0, 1, 2, 3, 4), **k}),
+    }
+
+
+_MATRIX, _OTHER = "contiguous bfloat16 matrix", "out has another shape, format or device"
+_REFUSED = [
+    ("quantize", lambda: {"X": _bf(4, 128).float()}, "X has to be a " + _MATRIX),
+    ("quantize", lambda: {"X": _bf(4, 256)[:, ::2]}, "X has to be a " + _MATRIX),
+    ("quantize", lambda: {"X": _bf(128, 4).t()}, "X has to be a " + _MATRIX),
+    ("quantize", lambda: {"X": _bf(128)}, "X has to be a " + _MATRIX),
+    ("quantize", lambda: {"X": _bf(1, 4, 128)}, "X has to be a " + _MATRIX),
+    ("quantize", lambda: {"X": _bf(4, 100)}, "cols % 32 == 0"),
+    ("quantize", lambda: {"format": 5}, "unknown MX format"),
+    ("quantize", lambda: {"out": _tensors(3, 128, b.MX_E4M3)}, _OTHER),
+    ("quantize", lambda: {"out": _tensors(4, 96, b.MX_E4M3)}, _OTHER),
+    ("quantize", lambda: {"out": _tensors(4, 128, b.MX_E2M1)}, _OTHER),
+    ("quantize", lambda: {"out": _tensors(4, 128, b.MX_E4M3, "meta")}, _OTHER),
+    ("dequantize", lambda: {"out": _bf(4, 64)}, "out has to be a contiguous bfloat16 tensor of shape"),
+    ("dequantize", lambda: {"out": _bf(3, 128)}, "out has to be"),
+    ("dequantize", lambda: {"out": _bf(4, 128).half()}, "out has to be"),
+    ("dequantize", lambda: {"out": _bf(4, 256)[:, ::2]}, "out has to be"),
+    ("dequantize", lambda: {"out": _bf(4, 128).to("meta")}, "out has to be"),
+    ("norm", lambda: {"X": _bf(4, 256)[:, ::2]}, "X has to be a " + _MATRIX),
+    ("norm", lambda: {"gamma": _bf(64)}, "gamma has to be"),
+    ("norm", lambda: {"gamma": _bf(1, 128)}, "gamma has to be"),
+    ("norm", lambda: {"gamma": _bf(128).float()}, "gamma has to be"),
+    ("norm", lambda: {"gamma": _bf(256)[::2]}, "gamma has to be"),
+    ("norm", lambda: {"gamma": _bf(128).to("meta")}, "gamma has to be"),
+    ("norm", lambda: {"residual": _bf(3, 128)}, "residual has to be"),
+    ("norm", lambda: {"residual": _bf(4, 128).float()}, "residual has to be"),
+    ("norm", lambda: {"residual": _bf(4, 128), "residual_out": _bf(4, 64)}, "residual_out has to be"),
+    ("norm", lambda: {"residual": _bf(4, 128), "residual_out": _bf(4, 128).float()}, "residual_out has to be"),
+    ("norm", lambda: {"out": _tensors(64, 128, b.MX_E4M3)}, _OTHER),
+    ("norm", lambda: {"out": _tensors(4, 128, b.MX_E2M1)}, _OTHER),
+    ("norm", lambda: {"X": _bf(4, 100), "gamma": _bf(100)}, "cols % 32 == 0"),
+]
+for _op in ("linear", "grouped"):
+    _REFUSED += [
+        (_op, lambda: {"x": _tensors(4, 64, b.MX_E4M3)}, "do not match a weight"),
+        (_op, lambda: {"x": _tensors(4, 128, b.MX_E4M3, "meta")}, "do not match a weight"),
+        (_op, lambda: {"x": _bf(4, 96)}, "do not match a weight"),
+        (_op, lambda: {"x": _bf(4, 128).to("meta")}, "do not match a weight"),
+        (_op, lambda: {"x": _bf(128)}, "x, where it is no MXTensor, has to be a " + _MATRIX),
+        (_op, lambda: {"x": _bf(4, 128).float()}, "has to be a " + _MATRIX),
+        (_op, lambda: {"x": _bf(4, 256)[:, ::2]}, "has to be a " + _MATRIX),
+        (_op, lambda: {"Y": _bf(3, 64)}, "Y has to be"),
+        (_op, lambda: {"Y": _bf(4, 32)}, "Y has to be"),
+        (_op, lambda: {"Y": _bf(4, 16).float()}, "Y has to be"),
+        (_op, lambda: {"Y": _bf(4, 128)[:, ::2]}, "Y has to be"),
+    ]
+_REFUSED += [
+    ("linear", lambda: {"Y": _bf(4, 64).to("meta")}, "Y has to be"),
+    ("grouped", lambda: {"Y": _bf(4, 16).to("meta")}, "Y has to be"),
+    ("grouped", lambda: {"Y": _bf(4, 64)}, "Y has to be"),
+    ("grouped", lambda: {"offsets": torch.zeros(5)}, "offsets have to be"),
+    ("grouped", lambda: {"offsets": torch.zeros(5, dtype=torch.int64)}, "offsets have to be"),
+    ("grouped", lambda: {"offsets": _offsets(0)}, "offsets have to be"),
+    ("grouped", lambda: {"offsets": _offsets(0, 1, 2, 3, 4).view(1, 5)}, "offsets have to be"),
+    ("grouped", lambda: {"offsets": _offsets(*range(10))[::2]}, "offsets have to be"),
+    ("grouped", lambda: {"offsets": _offsets(0, 1, 2, 3, 4).to("meta")}, "offsets have to be"),
+    ("grouped", lambda: {"offsets": _offsets(0, 1, 2, 3, 4, 4)}, "is not 5 experts of equal size"),
+    ("grouped", lambda: {"w": _tensors(0, 128, b.MX_E2M1)}, "is not 4 experts of equal size"),
+]
+_REFUSED += [(_op, lambda: {"stream": _StreamOfAnotherDevice()}, "the stream is of cuda:7")
+             for _op in ("quantize", "dequantize", "norm", "linear", "grouped")]
+
+
+@pytest.mark.parametrize("k", range(len(_REFUSED)))
+def test_each_refusal_of_the_binding_by_its_message(k, monkeypatch):
+    """The C calls get bare addresses, so the binding's checks are all that keeps a wrong shape from being read or written
+    out of range. Each is met with its own message, before anything reaches the library."""
+    def reached(*a):
+        raise _Reached()
+
+    monkeypatch.setattr(b, "_mx_run", reached)
+    op, args, message = _REFUSED[k]
+    with pytest.raises(ValueError, match=message):
+        _accepted()[op](**args())
+
+
+@pytest.mark.parametrize("op", ["quantize", "dequantize", "norm", "linear", "grouped"])
+def test_calls_without_a_fault_reach_the_library(op, monkeypatch):
+    """The calls that the refusals start from are refused for the device's type alone."""
+    with pytest.raises(ValueError, match="have to be on a CUDA device, not cpu"):
+        _accepted()[op]()
+
+    def reached(*a):
+        raise _Reached()
+
+    monkeypatch.setattr(b, "_mx_run", reached)
+    with pytest.raises(_Reached):
+        _accepted()[op]()
+    more = {"quantize": {"out": _tensors(4, 128, b.MX_E4M3)}, "dequantize": {"out": _bf(4, 128)},
+            "norm": {"residual": _bf(4, 128), "residual_out": _bf(4, 128), "out": _tensors(4, 128, b.MX_E4M3)},
+            "linear": {"x": _bf(4, 128), "Y": _bf(4, 64)}, "grouped": {"x": _bf(4, 128), "Y": _bf(4, 16)}}
+    with pytest.raises(_Reached):
+        _accepted()[op](**more[op])
