@@ -103,8 +103,9 @@ k_mx_quantize(const uint4* __restrict__ X, int64_t rows, int cols, uint8_t* __re
 
 // One thread decodes one block of 32 to 64 contiguous bytes of bf16. An element
 // times its scale has at most 4 significant bits, so fp32 and bf16 hold it
-// exactly except below bf16's smallest values (one rounding, nearest even). The
-// e2m1 codes go through the 16-entry table of the NF4 decoder.
+// exactly except below bf16's smallest values (one rounding, nearest even) and from
+// 2^128 on, which only imported storage reaches (infinite). The e2m1 codes go through the
+// 16-entry table of the NF4 decoder.
 template <int FMT, bool V8>
 __global__ void __launch_bounds__(kQuantThreads)
 k_mx_dequantize(const uint8_t* __restrict__ data, const uint8_t* __restrict__ scales, int64_t rows, int cols,

@@ -479,7 +479,9 @@ qlora_status qlora_quantize_mx(const void* X_bf16, const qlora_mx_tensor* q, qlo
 
 /* qlora_dequantize_mx -- element * 2^e to bf16 out [q->rows, q->cols] (16-byte
  * aligned). Exact, except that results below bf16's smallest normal number are
- * rounded to its subnormal ones (nearest, ties to even).
+ * rounded to its subnormal ones (nearest, ties to even), and that results of 2^128 or
+ * more, which no block of qlora_quantize_mx holds (E2M1 from byte 253, E4M3 from byte 247
+ * on), are infinities of the element's sign.
  * Errors: INVALID_ARG, UNSUPPORTED, ALIGNMENT, CUDA, DEVICE. */
 qlora_status qlora_dequantize_mx(const qlora_mx_tensor* q, void* out_bf16, qlora_stream_t stream);
 

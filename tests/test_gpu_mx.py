@@ -134,6 +134,24 @@ def test_dequantize_every_code_and_scale(fmt):
     assert np.isnan(_f64(got)[~fine]).all()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_dequantize_past_the_largest_bf16_value(fmt):
+    """Scale bytes that only imported storage has: results of 2^128 or more are infinities, those below are exact."""
+    dev = require_gpu()
+    table = mx.MAGNITUDES[fmt]
+    codes = np.zeros((16, 256), np.uint8)
+    codes[:, :len(table)] = np.arange(len(table))
+    codes[:, 128:128 + len(table)] = np.arange(len(table)) + mx.SIGN[fmt]
+    sc = np.repeat(np.arange(239, 255, dtype=np.uint8)[:, None], 8, 1)
+    data, scales = mx.pack(codes, sc, fmt)
+    got = b.qlora_dequantize_mx(b.MXTensor(torch.tensor(data).to(dev), torch.tensor(scales).to(dev), 16, 256, fmt))
+    _done()
+    ref = mx.dequantize(codes, sc, fmt)
+    big = np.abs(ref) >= 2.0 ** 128
+    assert big.any(1).tolist() == [byte >= (253 if fmt == b.MX_E2M1 else 247) for byte in range(239, 255)]
+    assert np.array_equal(_f64(got), np.where(big, np.copysign(np.inf, ref), ref))
+
+
 def test_rows_beyond_32_bit_offsets():
     """2.2e9 elements: the last rows are those of a small call."""
     dev = require_gpu()
