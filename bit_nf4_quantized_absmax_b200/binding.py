@@ -474,11 +474,6 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _BF16, _U8 = torch.bfloat16, torch.uint8
 
 
-def _require(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
 def _mx_bytes(rows: int, cols: int, format: int) -> tuple:
     """Bytes of data and scales (qlora_mx_storage_bytes, without a call)."""
     if cols <= 0 or cols % 32 or rows < 0:
