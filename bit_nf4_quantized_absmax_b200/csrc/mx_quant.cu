@@ -361,7 +361,10 @@ cudaError_t run_rmsnorm(const void* X, const void* residual, const void* gamma, 
   // 512 threads.
   const int chunks = nchunk_p <= 64 ? 1 : (nchunk_p <= 1024 ? 2 : 4);
   const int threads = ((nchunk_p + chunks - 1) / chunks + 31) / 32 * 32;
-  const int64_t resident = static_cast<int64_t>(num_sms) * (2048 / threads < 16 ? 2048 / threads : 16);
+  // As many CTAs as are resident: 59 to 64 registers a thread leave room for 1024 threads an SM. (With twice as many CTAs,
+  // half of them start when the others end, and each pays for gamma and its first row: 517x5152 e2m1 5.3 us, 4.8 so;
+  // 512x32768 23.8 and 21.3.)
+  const int64_t resident = static_cast<int64_t>(num_sms) * (1024 / threads < 16 ? 1024 / threads : 16);
   const int grid = static_cast<int>(q.rows < resident ? q.rows : resident);
   auto kern = chunks == 1 ? k_rmsnorm_mx<FMT, 1, RES> : (chunks == 2 ? k_rmsnorm_mx<FMT, 2, RES> : k_rmsnorm_mx<FMT, 4, RES>);
   return launch_pdl(kern, dim3(grid), dim3(threads), 0, stream, reinterpret_cast<const uint4*>(X),
