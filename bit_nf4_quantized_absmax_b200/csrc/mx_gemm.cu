@@ -668,7 +668,10 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
 // much for 256 (4096 tokens, 11008x4096: 234 us with those). The rows of a group are
 // cut into tiles of equal width, a multiple of 32, so no MMA is wider than its rows
 // need (8192 rows over 16 experts: 163 us with a remainder tile a group, 135 so).
-// What bounds it at full width is the MMA pipe: 2048 clocks for four k-blocks.
+// What bounds it at full width is the MMA pipe: 2048 clocks for four k-blocks, at the
+// 8-bit rate, whatever the format of the tokens (kind::mxf4 would multiply e2m1 by e2m1 at
+// twice the rate; it is not used). 384 threads leave 168 registers a thread, which all roles
+// share: k_mx_gemm_pair<2> spills 72 bytes there.
 //
 // The accumulator takes 256 TMEM columns and the scales 192 more, so there is one
 // accumulator; the epilogue's eight warps move it to registers (rounded to bf16, 64
@@ -1227,6 +1230,10 @@ static int64_t rows_per_group(int64_t M, int64_t groups) {
   return used > 0 ? (M + used - 1) / used : 0;
 }
 
+// Every choice goes by the average group, since the offsets are on the device: with 512 rows of 64 experts, 2048x2048, all
+// at one expert the call takes 29 us in 32 tiles of 16 tokens, where that expert's product alone would take 12 (and 43 with
+// 8 rows at each).
+//
 // Most rows of a group, on average, for tiles of 16 tokens: groups are uneven, and a group that needs two tiles reads its
 // weights twice (64 experts, 2048x2048, 500 rows: 42.5 us in tiles of 16, 41.2 of 32; 1000 rows: 58.8 and 44.7; 16
 // experts, 4096x4096, 200 rows: 43.8 and 34.5).

@@ -1,5 +1,7 @@
 // Conversion of bf16 matrices to MX storage and back, and the RMS norm whose
-// output is MX. All of it is bound by memory traffic.
+// output is MX. Conversion is bound by memory traffic (6.1 TB/s at 11008x4096), and so is
+// nearly the norm with a residual at its largest (4096x4096: 5.2 TB/s); below that a norm
+// is bound by the latency of a row and its sum.
 //
 // Storage of [rows, cols] (cols % 32 == 0; kp = cols rounded up to 128):
 //   data   : [rows][kp] e4m3 bytes, or [rows][kp / 2] bytes of two e2m1 codes
@@ -356,9 +358,11 @@ template <int FMT, bool RES>
 cudaError_t run_rmsnorm(const void* X, const void* residual, const void* gamma, float eps, const MxView& q,
                         void* residual_out, int num_sms, cudaStream_t stream) {
   const int nchunk_p = static_cast<int>((q.cols + 127) / 128 * 16);
-  // Two chunks a thread halve what a row's sum costs against its elements (4096x4096 with a residual: 23.9 us with one,
-  // 22.5 with two, 33.1 with four, whose registers leave half of the threads); four only where two would need more than
-  // 512 threads.
+  // Two chunks a thread halve what a row's sum costs against its elements (4096x4096 with a residual: 24.8 us with one,
+  // 22.8 with two, 33.3 with four, of which 224 bytes a thread are spilled at 64 registers), but narrow rows have too few
+  // threads then (8192x256: 5.4 us with one, 6.5 with two). Four where two would need more than 512 threads, and must
+  // where they would need more than 1024. (Between the two limits two are faster: 1024x12288 18.8 us and 25.5 with four,
+  // 1024x16384 23.5 and 33.7.)
   const int chunks = nchunk_p <= 64 ? 1 : (nchunk_p <= 1024 ? 2 : 4);
   const int threads = ((nchunk_p + chunks - 1) / chunks + 31) / 32 * 32;
   // As many CTAs as are resident: 59 to 64 registers a thread leave room for 1024 threads an SM. (With twice as many CTAs,

@@ -172,6 +172,8 @@ def test_rows_beyond_32_bit_offsets():
 
 
 # ---- RMS norm ----
+# (The kernel's sums are fp64, so the bound that follows, of sums in fp32, holds with room to spare; the narrow one stands at
+# test_rmsnorm_codes_of_the_exact_value.)
 # A thread adds at most 32 squares in fp32 (each addition off by 2^-24 of the partial sum, all terms positive: the sum
 # within 32 * 2^-24 relative), which the root halves; the fp64 steps and the tail of rstd add less than 2^-40, and y is
 # rounded once to fp32 (2^-24): 17 * 2^-24 covers it.
