@@ -442,12 +442,12 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
   const int kb1 = static_cast<int>(static_cast<int64_t>(a.nkb) * (rank + 1) / S);
 
   if (tt.found) {  // the same in every thread of the cluster
+    int issued = 0;  // copies, in the thread that issues them
     if (warp == 0) {
       const uint32_t bytes = C::W_BYTES / 2 + (QUANT ? 0 : a.x_fp4 ? C::X_BYTES / 2 : C::X_BYTES);
       const int32_t wrow = static_cast<int32_t>(w0), xrow = static_cast<int32_t>(tt.row0);
       if (elect_one()) {
         bool ok = true;
-        int issued = 0;
         for (int round = 0, kb = kb0; kb < kb1 && ok; ++round) {
 #pragma unroll
           for (int st = 0; st < C::STAGES; ++st, ++kb) {
@@ -464,10 +464,6 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
             }
           }
         }
-        // after an abort, let the copies already issued land before the CTA leaves
-        if (*abort_flag)
-          for (int i = max(0, issued - C::STAGES); i < issued; ++i)
-            mbar_wait_bounded(&full[i % C::STAGES], (i / C::STAGES) & 1, err, DEV_TIMEOUT_TMA_FULL);
       }
     } else if (warp == 1) {
       const uint32_t s0 = smem_u32(smem);
@@ -563,6 +559,9 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUte
     __syncwarp();
 
     const bool ok = wait_or_abort(accf, 0, abort_flag, err, DEV_TIMEOUT_ACCUM);
+    if (!ok)  // whichever role gave up: the copies already issued land before the CTA leaves
+      for (int i = max(0, issued - C::STAGES); i < issued; ++i)
+        mbar_wait_bounded(&full[i % C::STAGES], (i / C::STAGES) & 1, err, DEV_TIMEOUT_TMA_FULL);
     tc_fence_after();
     const int tokens = static_cast<int>(min(static_cast<int64_t>(TN), tt.end - tt.row0));
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -942,8 +941,8 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         }
       }
     }
-    // after an abort, let the copies already issued land before the pair leaves
-    if (leader && rank == 0 && *abort_flag)
+    // The copies issued last, of both CTAs, land before the pair leaves, also where another role gives up after this one.
+    if (leader && rank == 0)
       for (int64_t i = max(static_cast<int64_t>(0), issued - a.stages); i < issued; ++i)
         mbar_wait_bounded(&full[i % a.stages], (i / a.stages) & 1, err, DEV_TIMEOUT_TMA_FULL);
   } else if (warp == 1) {
